@@ -32,11 +32,40 @@ gdr_status ok() {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned_to(const void *p, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+bool aligned4(const void *p) { return aligned_to(p, 4); }
+
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
 gdr_status from_cuda(cudaError_t e, const char *what) {
   if (e == cudaSuccess) return ok();
   return fail(GDR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+gdr_status check_kinds(gdr_dtype in_dtype, gdr_gate_kind gate, int norm_qk) {
+  if (in_dtype != GDR_F32 && in_dtype != GDR_BF16)
+    return fail(GDR_ERR_INVALID_ARG, "in_dtype must be GDR_F32 or GDR_BF16");
+  if (gate != GDR_GATE_SCALAR && gate != GDR_GATE_PER_CHANNEL)
+    return fail(GDR_ERR_INVALID_ARG, "unknown gate kind");
+  if (norm_qk < 0 || norm_qk > 3) return fail(GDR_ERR_INVALID_ARG, "norm_qk must be 0..3");
+  return GDR_OK;
+}
+
+// A distance between rows of `width` elements: no overlap, whole 16-byte units.
+gdr_status check_stride(const char *name, long long stride, long long width, long long rows,
+                        gdr_dtype dtype) {
+  if (rows <= 1) return GDR_OK;  // (never multiplied by more than zero)
+  if (stride < width)
+    return fail(GDR_ERR_INVALID_ARG, "%s stride %lld is less than a row's %lld elements", name,
+                stride, width);
+  if (stride % (dtype == GDR_BF16 ? 8 : 4) != 0)
+    return fail(GDR_ERR_INVALID_ARG, "%s stride %lld is not a multiple of 16 bytes", name, stride);
+  if (stride > (1ll << 40) / rows)
+    return fail(GDR_ERR_INVALID_ARG, "%s stride %lld: problem too large", name, stride);
+  return GDR_OK;
 }
 
 // Number of SMs of the current device (cached per device; 0 if unknown).
@@ -113,6 +142,7 @@ const char *gdr_status_string(gdr_status s) {
     case GDR_ERR_CUDA: return "GDR_ERR_CUDA";
     case GDR_ERR_TIMEOUT: return "GDR_ERR_TIMEOUT";
     case GDR_ERR_RANGE: return "GDR_ERR_RANGE";
+    case GDR_ERR_SLOT: return "GDR_ERR_SLOT";
   }
   return "GDR_ERR_UNKNOWN";
 }
@@ -489,6 +519,256 @@ gdr_status gdr_step(const void *q, const void *k, const void *v, gdr_dtype in_dt
                    "gdr_step launch");
 }
 
+gdr_status gdr_step_slots(const void *q, const void *k, const void *v, gdr_dtype in_dtype,
+                          long long q_stride, long long k_stride, long long v_stride,
+                          const float *g, gdr_gate_kind gate, const float *beta,
+                          const float *gate_scale, int norm_qk, float *pool, int slots,
+                          long long slot_stride, const int *src, const int *dst,
+                          const int *cu_seqlens, void *o, int R, int total, int Hk, int H,
+                          int dk, int dv, gdr_stream_t stream) {
+  if (R < 0 || total < 0 || Hk < 0 || H < 0 || slots < 0)
+    return fail(GDR_ERR_INVALID_ARG, "negative R/total/Hk/H/slots");
+  gdr_status st = check_kinds(in_dtype, gate, norm_qk);
+  if (st != GDR_OK) return st;
+  if (!head_dim_ok(dk) || !head_dim_ok(dv))
+    return fail(GDR_ERR_UNSUPPORTED, "head dims dk=%d dv=%d (need 32, 64 or 128)", dk, dv);
+  if ((size_t)R * H == 0 || total == 0) return ok();
+  if (Hk == 0 || H % Hk != 0)
+    return fail(GDR_ERR_INVALID_ARG, "H=%d is not a multiple of Hk=%d", H, Hk);
+  if (!cu_seqlens && total != R)
+    return fail(GDR_ERR_INVALID_ARG, "without cu_seqlens total=%d must be R=%d", total, R);
+  if (!q || !k || !v || !g || !beta || !src || !o || (slots && !pool))
+    return fail(GDR_ERR_INVALID_ARG, "null q/k/v/g/beta/pool/src/o");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) ||
+      !aligned16(gate_scale) || !aligned16(pool) || !aligned16(o))
+    return fail(GDR_ERR_INVALID_ARG, "q/k/v/g/beta/gate_scale/pool/o must be 16-byte aligned");
+  if (!aligned4(src) || !aligned4(dst) || !aligned4(cu_seqlens))
+    return fail(GDR_ERR_INVALID_ARG, "src/dst/cu_seqlens must be 4-byte aligned");
+  st = check_stride("q", q_stride, (long long)Hk * dk, total, in_dtype);
+  if (st == GDR_OK) st = check_stride("k", k_stride, (long long)Hk * dk, total, in_dtype);
+  if (st == GDR_OK) st = check_stride("v", v_stride, (long long)H * dv, total, in_dtype);
+  if (st == GDR_OK) st = check_stride("pool", slot_stride, (long long)H * dv * dk, slots, GDR_F32);
+  if (st != GDR_OK) return st;
+  if ((size_t)R * H > (size_t)1 << 28) return fail(GDR_ERR_INVALID_ARG, "R*H too large");
+  gdr::StepSlotsArgs a{};
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.g = g; a.beta = beta; a.gate_scale = gate_scale; a.norm_qk = norm_qk;
+  a.pool = pool; a.slots = slots; a.slot_stride = slot_stride;
+  a.src = src; a.dst = dst; a.cu = cu_seqlens; a.o = o;
+  a.R = R; a.total = total; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv;
+  a.bf16 = in_dtype == GDR_BF16;
+  a.per_channel = gate == GDR_GATE_PER_CHANNEL;
+  cudaError_t e = status_word(&a.status);
+  if (e != cudaSuccess) return from_cuda(e, "gdr_step_slots status word");
+  return from_cuda(gdr::launch_step_slots(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "gdr_step_slots launch");
+}
+
+gdr_status gdr_slot_map(const int *lens, const int *kept, const int *table,
+                        long long table_stride, int R, int W, int slots, int max_tokens,
+                        int keep_all, int *cu_seqlens, int *request, int *src, int *dst,
+                        gdr_stream_t stream) {
+  if (R < 0 || slots < 0 || max_tokens < 0)
+    return fail(GDR_ERR_INVALID_ARG, "negative R/slots/max_tokens");
+  if (R > 65536) return fail(GDR_ERR_UNSUPPORTED, "R=%d requests (at most 65536)", R);
+  if (W < 1) return fail(GDR_ERR_INVALID_ARG, "W=%d slots a request (need at least 1)", W);
+  if (keep_all != 0 && keep_all != 1) return fail(GDR_ERR_INVALID_ARG, "keep_all must be 0 or 1");
+  if (R > 1 && table_stride < W)
+    return fail(GDR_ERR_INVALID_ARG, "table_stride=%lld is less than W=%d", table_stride, W);
+  if (!cu_seqlens || (R && (!lens || !kept || !table || !src)) ||
+      (max_tokens && (!request || !dst)))
+    return fail(GDR_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned4(lens) || !aligned4(kept) || !aligned4(table) || !aligned4(cu_seqlens) ||
+      !aligned4(request) || !aligned4(src) || !aligned4(dst))
+    return fail(GDR_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+  gdr::SlotMapArgs a{};
+  a.lens = lens; a.kept = kept; a.table = table; a.table_stride = table_stride;
+  a.R = R; a.W = W; a.slots = slots; a.max_tokens = max_tokens; a.keep_all = keep_all;
+  a.cu = cu_seqlens; a.request = request; a.src = src; a.dst = dst;
+  cudaError_t e = status_word(&a.status);
+  if (e != cudaSuccess) return from_cuda(e, "gdr_slot_map status word");
+  return from_cuda(gdr::launch_slot_map(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "gdr_slot_map launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by both directions of the output norm; fills the arguments.
+gdr_status check_group_norm(const void *x, const void *z, gdr_dtype dtype, long long x_stride,
+                            long long z_stride, const float *weight, const float *bias,
+                            int per_channel, gdr_act act, int center, float eps, long long rows,
+                            int G, int D, gdr::GroupNormArgs *out) {
+  if (rows < 0 || G < 1 || D < 1) return fail(GDR_ERR_INVALID_ARG, "rows < 0, G < 1 or D < 1");
+  if (dtype != GDR_F32 && dtype != GDR_BF16)
+    return fail(GDR_ERR_INVALID_ARG, "dtype must be GDR_F32 or GDR_BF16");
+  if (act != GDR_ACT_NONE && act != GDR_ACT_SILU && act != GDR_ACT_SIGMOID)
+    return fail(GDR_ERR_INVALID_ARG, "unknown activation");
+  if (per_channel != 0 && per_channel != 1)
+    return fail(GDR_ERR_INVALID_ARG, "per_channel must be 0 or 1");
+  if (!(eps > 0.f) || eps > 1e30f) return fail(GDR_ERR_INVALID_ARG, "eps must be positive");
+  if (D > 1024 || (long long)G * D > 65536)
+    return fail(GDR_ERR_UNSUPPORTED, "G=%d groups of D=%d (D <= 1024, G*D <= 65536)", G, D);
+  if (rows > (1ll << 40)) return fail(GDR_ERR_INVALID_ARG, "problem too large");
+  const size_t size = dtype == GDR_BF16 ? 2 : 4;
+  if (rows && !x) return fail(GDR_ERR_INVALID_ARG, "null x");
+  if (!aligned_to(x, size) || !aligned_to(z, size) || !aligned4(weight) || !aligned4(bias))
+    return fail(GDR_ERR_INVALID_ARG, "x/z/weight/bias must be aligned to their elements");
+  if (rows > 1 && (x_stride < (long long)G * D || (z && z_stride < (long long)G * D)))
+    return fail(GDR_ERR_INVALID_ARG, "x_stride/z_stride less than G*D=%lld", (long long)G * D);
+  gdr::GroupNormArgs a{};
+  a.x = x; a.z = z; a.x_stride = x_stride; a.z_stride = z_stride;
+  a.weight = weight; a.bias = bias; a.per_channel = per_channel; a.act = act;
+  a.center = center != 0; a.eps = eps; a.rows = rows; a.G = G; a.D = D;
+  a.bf16 = dtype == GDR_BF16;
+  *out = a;
+  return ok();
+}
+
+// Checks shared by both directions of the prologue; fills the arguments.
+gdr_status check_prologue(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
+                          long long k_stride, const float *a, gdr_gate_kind gate, const float *b,
+                          const float *gate_scale, int norm_qk, long long tokens, int Hk, int H,
+                          int dk, gdr::PrologueArgs *out) {
+  if (tokens < 0 || Hk < 1 || H < 1) return fail(GDR_ERR_INVALID_ARG, "tokens < 0, Hk < 1 or H < 1");
+  gdr_status st = check_kinds(in_dtype, gate, norm_qk);
+  if (st != GDR_OK) return st;
+  if (!head_dim_ok(dk)) return fail(GDR_ERR_UNSUPPORTED, "head dim dk=%d (need 32, 64 or 128)", dk);
+  if (H % Hk != 0) return fail(GDR_ERR_INVALID_ARG, "H=%d is not a multiple of Hk=%d", H, Hk);
+  if (H > 65536) return fail(GDR_ERR_UNSUPPORTED, "H=%d heads (at most 65536)", H);
+  if (tokens > (1ll << 40) / H) return fail(GDR_ERR_INVALID_ARG, "problem too large");
+  if (tokens && (!q || !k || !a || !b || !gate_scale))
+    return fail(GDR_ERR_INVALID_ARG, "null q/k/a/b/gate_scale");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(a) || !aligned16(b) || !aligned16(gate_scale))
+    return fail(GDR_ERR_INVALID_ARG, "q/k/a/b/gate_scale must be 16-byte aligned");
+  st = check_stride("q", q_stride, (long long)Hk * dk, tokens, in_dtype);
+  if (st == GDR_OK) st = check_stride("k", k_stride, (long long)Hk * dk, tokens, in_dtype);
+  if (st != GDR_OK) return st;
+  gdr::PrologueArgs p{};
+  p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride;
+  p.a = a; p.b = b; p.gate_scale = gate_scale; p.norm_qk = norm_qk;
+  p.tokens = tokens; p.Hk = Hk; p.H = H; p.d = dk;
+  p.bf16 = in_dtype == GDR_BF16;
+  p.per_channel = gate == GDR_GATE_PER_CHANNEL;
+  *out = p;
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+gdr_status gdr_group_norm_fwd(const void *x, const void *z, gdr_dtype dtype, long long x_stride,
+                              long long z_stride, const float *weight, const float *bias,
+                              int per_channel, gdr_act act, int center, float eps, void *y,
+                              long long rows, int G, int D, gdr_stream_t stream) {
+  gdr::GroupNormArgs a;
+  gdr_status st = check_group_norm(x, z, dtype, x_stride, z_stride, weight, bias, per_channel, act,
+                                   center, eps, rows, G, D, &a);
+  if (st != GDR_OK) return st;
+  if (rows == 0) return ok();
+  if (!y) return fail(GDR_ERR_INVALID_ARG, "null y");
+  if (!aligned_to(y, a.bf16 ? 2 : 4))
+    return fail(GDR_ERR_INVALID_ARG, "y must be aligned to its elements");
+  a.y = y;
+  return from_cuda(gdr::launch_group_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "gdr_group_norm_fwd launch");
+}
+
+size_t gdr_group_norm_bwd_workspace_bytes(long long rows, int G, int D, gdr_dtype dtype,
+                                          int per_channel) {
+  if (rows < 0 || G < 1 || D < 1 || D > 1024 || (long long)G * D > 65536 || rows > (1ll << 40))
+    return 0;
+  return gdr::group_norm_bwd_ws_bytes(rows, G, D, dtype == GDR_BF16, per_channel);
+}
+
+gdr_status gdr_group_norm_bwd(const void *dy, const void *x, const void *z, gdr_dtype dtype,
+                              long long x_stride, long long z_stride, const float *weight,
+                              const float *bias, int per_channel, gdr_act act, int center,
+                              float eps, float *dx, void *dz, float *dweight, float *dbias,
+                              long long rows, int G, int D, void *workspace, size_t ws_bytes,
+                              gdr_stream_t stream) {
+  gdr::GroupNormArgs a;
+  gdr_status st = check_group_norm(x, z, dtype, x_stride, z_stride, weight, bias, per_channel, act,
+                                   center, eps, rows, G, D, &a);
+  if (st != GDR_OK) return st;
+  if (dz && !z) return fail(GDR_ERR_INVALID_ARG, "dz without z");
+  if (rows && (!dy || !dx)) return fail(GDR_ERR_INVALID_ARG, "null dy/dx");
+  const size_t size = a.bf16 ? 2 : 4;
+  if (!aligned_to(dy, size) || !aligned_to(dz, size) || !aligned4(dx) || !aligned4(dweight) ||
+      !aligned4(dbias))
+    return fail(GDR_ERR_INVALID_ARG, "dy/dx/dz/dweight/dbias must be aligned to their elements");
+  if (dweight || dbias) {
+    const size_t need = gdr_group_norm_bwd_workspace_bytes(rows, G, D, dtype, per_channel);
+    if (ws_bytes < need || !workspace)
+      return fail(GDR_ERR_WORKSPACE, "workspace %zu B < required %zu B", ws_bytes, need);
+    if (!aligned16(workspace))
+      return fail(GDR_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  } else if (rows == 0) {
+    return ok();
+  }
+  a.dy = dy; a.dx = dx; a.dz = dz; a.dweight = dweight; a.dbias = dbias;
+  a.ws = static_cast<float *>(workspace);
+  return from_cuda(gdr::launch_group_norm_bwd(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "gdr_group_norm_bwd launch");
+}
+
+gdr_status gdr_prologue_fwd(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
+                            long long k_stride, const float *a, gdr_gate_kind gate,
+                            const float *b, const float *gate_scale, int norm_qk, void *qn,
+                            void *kn, float *g, float *beta, long long tokens, int Hk, int H,
+                            int dk, gdr_stream_t stream) {
+  gdr::PrologueArgs p;
+  gdr_status st = check_prologue(q, k, in_dtype, q_stride, k_stride, a, gate, b, gate_scale,
+                                 norm_qk, tokens, Hk, H, dk, &p);
+  if (st != GDR_OK) return st;
+  if (tokens == 0) return ok();
+  if (!qn || !kn || !g || !beta) return fail(GDR_ERR_INVALID_ARG, "null qn/kn/g/beta");
+  if (!aligned16(qn) || !aligned16(kn) || !aligned16(g) || !aligned16(beta))
+    return fail(GDR_ERR_INVALID_ARG, "qn/kn/g/beta must be 16-byte aligned");
+  p.qn = qn; p.kn = kn; p.g = g; p.beta = beta;
+  return from_cuda(gdr::launch_prologue_fwd(p, reinterpret_cast<cudaStream_t>(stream)),
+                   "gdr_prologue_fwd launch");
+}
+
+size_t gdr_prologue_bwd_workspace_bytes(long long tokens, int H, int dk, gdr_gate_kind gate) {
+  if (tokens < 0 || H < 1 || H > 65536 || !head_dim_ok(dk) || tokens > (1ll << 40) / H) return 0;
+  return gdr::prologue_bwd_ws_bytes(tokens, H, dk, gate == GDR_GATE_PER_CHANNEL);
+}
+
+gdr_status gdr_prologue_bwd(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
+                            long long k_stride, const float *a, gdr_gate_kind gate,
+                            const float *b, const float *gate_scale, int norm_qk,
+                            const float *dqn, const float *dkn, const float *dg,
+                            const float *dbeta, void *dq, void *dk_, float *da, float *db,
+                            float *dgate_scale, long long tokens, int Hk, int H, int dk,
+                            void *workspace, size_t ws_bytes, gdr_stream_t stream) {
+  gdr::PrologueArgs p;
+  gdr_status st = check_prologue(q, k, in_dtype, q_stride, k_stride, a, gate, b, gate_scale,
+                                 norm_qk, tokens, Hk, H, dk, &p);
+  if (st != GDR_OK) return st;
+  if (!dgate_scale || (tokens && (!dqn || !dkn || !dg || !dbeta || !dq || !dk_ || !da || !db)))
+    return fail(GDR_ERR_INVALID_ARG, "null gradient pointer");
+  if (!aligned16(dqn) || !aligned16(dkn) || !aligned16(dg) || !aligned16(dbeta) ||
+      !aligned16(dq) || !aligned16(dk_) || !aligned16(da) || !aligned16(db) ||
+      !aligned16(dgate_scale))
+    return fail(GDR_ERR_INVALID_ARG, "gradients must be 16-byte aligned");
+  const size_t need = gdr_prologue_bwd_workspace_bytes(tokens, H, dk, gate);
+  if (ws_bytes < need || !workspace)
+    return fail(GDR_ERR_WORKSPACE, "workspace %zu B < required %zu B", ws_bytes, need);
+  if (!aligned16(workspace)) return fail(GDR_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (tokens == 0)  // no tokens: the sum over them is zero
+    return from_cuda(cudaMemsetAsync(dgate_scale, 0, (size_t)H * sizeof(float), s),
+                     "gdr_prologue_bwd clear");
+  p.dqn = dqn; p.dkn = dkn; p.dg = dg; p.dbeta = dbeta;
+  p.dq = dq; p.dk = dk_; p.da = da; p.db = db; p.dgate_scale = dgate_scale;
+  p.ws = static_cast<float *>(workspace);
+  return from_cuda(gdr::launch_prologue_bwd(p, s), "gdr_prologue_bwd launch");
+}
+
 gdr_status gdr_testing_skip_stage_load(int chunk) {
   if (chunk < 0) return fail(GDR_ERR_INVALID_ARG, "chunk must be >= 0");
   t_skip_stage_chunk = chunk;
@@ -512,6 +792,11 @@ gdr_status gdr_get_device_status(gdr_stream_t stream) {
                 "a per-channel gate decayed beyond the tensor-core path's range (more than "
                 "about 83 in log decay over half a chunk); those results are not valid "
                 "(status word 0x%x)",
+                word);
+  if (word & gdr::kStatusSlot)
+    return fail(GDR_ERR_SLOT,
+                "a request named a state slot, a length or a kept count that does not exist; it "
+                "was skipped (status word 0x%x)",
                 word);
   return ok();
 }

@@ -16,6 +16,8 @@ constexpr unsigned int kStatusTimeout = 1u;
 // A per-channel gate decayed faster than the tensor-core path's tile scaling
 // can represent in some chunk (that call's results are not the recurrence's).
 constexpr unsigned int kStatusRange = 2u;
+// A request named a state slot, a length or a kept count that does not exist.
+constexpr unsigned int kStatusSlot = 4u;
 
 struct ChunkArgs {
   const void *q, *k, *v;
@@ -74,8 +76,75 @@ struct StepArgs {
   unsigned int *status;
 };
 
+// The recurrent form over a pool of state slots (see gdr_step_slots).
+struct StepSlotsArgs {
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  const float *g, *beta;
+  const float *gate_scale;  // null: g, beta are ready
+  int norm_qk;
+  float *pool;
+  long long slot_stride;
+  int slots;
+  const int *src, *dst, *cu;
+  void *o;
+  int R, total, Hk, H, dk, dv;
+  int bf16, per_channel;
+  unsigned int *status;
+};
+
+struct SlotMapArgs {
+  const int *lens, *kept, *table;
+  long long table_stride;
+  int R, W, slots, max_tokens, keep_all;
+  int *cu, *request, *src, *dst;
+  unsigned int *status;
+};
+
+// Group norm, channels last, with an activation (dy null: forward).
+struct GroupNormArgs {
+  const void *x, *z, *dy;
+  long long x_stride, z_stride;  // elements between rows
+  const float *weight, *bias;
+  int per_channel, act, center;
+  float eps;
+  void *y;    // forward
+  float *dx;  // backward
+  void *dz;
+  float *dweight, *dbias;
+  float *ws;
+  long long rows;
+  int G, D;
+  int bf16;
+};
+
+// The prologue as a map of its own (dqn null: forward).
+struct PrologueArgs {
+  const void *q, *k;
+  long long q_stride, k_stride;  // elements between tokens
+  const float *a, *b, *gate_scale;
+  int norm_qk;
+  void *qn, *kn;  // forward
+  float *g, *beta;
+  const float *dqn, *dkn, *dg, *dbeta;  // backward
+  void *dq, *dk;
+  float *da, *db, *dgate_scale;
+  float *ws;
+  long long tokens;
+  int Hk, H, d;
+  int bf16, per_channel;
+};
+
 // Launchers return cudaSuccess or the launch error.
 cudaError_t launch_step(const StepArgs &a, cudaStream_t stream);
+cudaError_t launch_step_slots(const StepSlotsArgs &a, cudaStream_t stream);
+cudaError_t launch_slot_map(const SlotMapArgs &a, cudaStream_t stream);
+size_t group_norm_bwd_ws_bytes(long long rows, int G, int D, int bf16, int per_channel);
+cudaError_t launch_group_norm_fwd(const GroupNormArgs &a, cudaStream_t stream);
+cudaError_t launch_group_norm_bwd(const GroupNormArgs &a, cudaStream_t stream);
+size_t prologue_bwd_ws_bytes(long long tokens, int H, int dk, int per_channel);
+cudaError_t launch_prologue_fwd(const PrologueArgs &a, cudaStream_t stream);
+cudaError_t launch_prologue_bwd(const PrologueArgs &a, cudaStream_t stream);
 // Split-operand tensor-core forward (fp32 inputs, and head dims the
 // warp-specialised kernel does not take): every operand as two bf16 terms,
 // every product as three MMAs; returns cudaErrorNotSupported outside its

@@ -31,7 +31,8 @@
  * - A kernel that gives up a bounded wait records GDR_ERR_TIMEOUT in a
  *   device status word; gdr_get_device_status() reads and clears it.  The
  *   tensor-core path records GDR_ERR_RANGE there when a per-channel gate
- *   decays beyond what it can represent (see gdr_chunk_fwd).
+ *   decays beyond what it can represent (see gdr_chunk_fwd), and the pooled
+ *   decode records GDR_ERR_SLOT for slots that do not exist.
  * - Gate: `g` holds log(alpha) in fp32 (finite, <= 0).  A scalar gate has one
  *   value per (token, head); a per-channel gate has d_k values.
  * - Dtypes: q, k, v and o share `in_dtype` (fp32 or bf16); g, beta and the
@@ -39,7 +40,8 @@
  * - No query scale is applied: o_t = S_t q_t exactly as written above.
  * - Supported head sizes: d_k, d_v in {32, 64, 128}.  Chunk size C = 64.
  * - Pointers must be 16-byte aligned; every tensor is dense row-major
- *   (contiguous) in the layout given below.
+ *   (contiguous) in the layout given below, except where an entry point takes
+ *   strides.
  */
 #ifndef GDR_H_
 #define GDR_H_
@@ -57,8 +59,10 @@ typedef enum {
   GDR_ERR_WORKSPACE = 3,   /* workspace pointer/size too small              */
   GDR_ERR_CUDA = 4,        /* a CUDA runtime call failed                    */
   GDR_ERR_TIMEOUT = 5,     /* a kernel gave up a bounded wait (device word) */
-  GDR_ERR_RANGE = 6        /* per-channel decay beyond the tensor-core path's
+  GDR_ERR_RANGE = 6,       /* per-channel decay beyond the tensor-core path's
                               range in some chunk (device word)             */
+  GDR_ERR_SLOT = 7         /* a request named a state slot, a length or a kept
+                              count that does not exist (device word)       */
 } gdr_status;
 
 typedef enum { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -387,13 +391,197 @@ gdr_status gdr_step(const void *q, const void *k, const void *v, gdr_dtype in_dt
                     const float *g, gdr_gate_kind gate, const float *beta, float *S, void *o,
                     int N, int H, int dk, int dv, gdr_stream_t stream);
 
+/* Values of src (gdr_step_slots, gdr_slot_map) that are not a slot. */
+#define GDR_SLOT_ZERO (-1) /* the request is new: it starts from a zero state */
+#define GDR_SLOT_SKIP (-2) /* the request is not run: nothing of it is touched */
+
+/*
+ * The recurrent form over a pool of state slots, for serving: R requests of
+ * one or more tokens each, every request's state read from the slot it names
+ * and written to the slots it names.  Source as gdr_step; the maps from raw
+ * projections are those of gdr_chunk_fwd_prologue.
+ *
+ * Request r runs tokens [cu_seqlens[r], cu_seqlens[r + 1]) of the packed
+ * tensors in order.  Per value head h, with key head h / (H / Hk):
+ *
+ *   S = pool[src[r], h]                     (or 0)
+ *   per token t: decay, erase, write, o_t = S q_t as in gdr_step,
+ *                then pool[dst[t], h] = S   if dst[t] >= 0
+ *
+ *   q, k   [total, Hk, dk] in_dtype   rows q_stride / k_stride elements apart
+ *                                     (the heads of a token are contiguous)
+ *   v      [total, H, dv]  in_dtype   rows v_stride elements apart
+ *   g      [total, H] or [total, H, dk] fp32; beta [total, H] fp32: log alpha
+ *          and the write strength if gate_scale is NULL, else the logits a, b
+ *          (g = -gate_scale[h] softplus(a), beta = sigmoid(b))
+ *   gate_scale  [H] fp32 or NULL
+ *   norm_qk     GDR_NORM_Q | GDR_NORM_K: L2-normalise q, k in the kernel
+ *   pool   [slots, H, dv, dk] fp32    slots slot_stride elements apart
+ *   src    [R] int32    the slot whose state request r starts from, or
+ *                       GDR_SLOT_ZERO, or GDR_SLOT_SKIP
+ *   dst    [total] int32 or NULL      the slot that keeps the state after
+ *          token t (-1: not kept).  NULL: the state after a request's last
+ *          token goes back to src[r] (and is dropped if src[r] is
+ *          GDR_SLOT_ZERO)
+ *   cu_seqlens  [R + 1] int32 or NULL (then total == R, one token a request);
+ *          values are clamped into [0, total]; a request without tokens
+ *          touches nothing
+ *   o      [total, H, dv] in_dtype    dense; rows that no request covers and
+ *          rows of skipped requests are left as they were
+ *
+ * A slot that a request writes (dst, or src with dst NULL) may be named by no
+ * other request of the call; requests that only read may share a slot (a
+ * fork), and one request may name its slots in any order and more than once
+ * (the last write stays).  A src beyond the pool skips its request and a dst
+ * beyond the pool is not written; both record GDR_ERR_SLOT in the device
+ * status word.
+ *
+ * dk, dv in {32, 64, 128}; H a multiple of Hk; pointers 16-byte aligned
+ * (int32 arrays 4-byte), strides multiples of 16 bytes.  Any length runs, one
+ * token after the other; from some tens of tokens a request on, the chunked
+ * forward is the faster one.  fp32 arithmetic, o rounded once.  One launch, no
+ * workspace; the arrays may not overlap, src aside (it may be dst).
+ */
+gdr_status gdr_step_slots(const void *q, const void *k, const void *v, gdr_dtype in_dtype,
+                          long long q_stride, long long k_stride, long long v_stride,
+                          const float *g, gdr_gate_kind gate, const float *beta,
+                          const float *gate_scale, int norm_qk, float *pool, int slots,
+                          long long slot_stride, const int *src, const int *dst,
+                          const int *cu_seqlens, void *o, int R, int total, int Hk, int H,
+                          int dk, int dv, gdr_stream_t stream);
+
+/*
+ * The maps gdr_step_slots and gdr_chunk_fwd_varlen read, built on the GPU
+ * from the requests' lengths, so that lengths and kept counts that a kernel
+ * wrote (drafts, and how many of them were accepted) never visit the host.
+ *
+ *   lens   [R] int32   new tokens of each request, >= 0
+ *   kept   [R] int32   0: the request has no state yet; n: it goes on from
+ *                      the state in table[r, n - 1] (with keep_all, the state
+ *                      after token n of its last call), n <= W
+ *   table  [R, W] int32  the slots that belong to each request, rows
+ *                      table_stride elements apart
+ *   keep_all  1: the state after token j is kept in table[r, j] (lens <= W);
+ *             0: only the state after a request's last token, in table[r, 0]
+ *   cu_seqlens [R + 1], src [R], request [max_tokens], dst [max_tokens]
+ *             (written, int32): offsets, start slots, the request of each
+ *             token and the slot its state goes to.  Entries behind the last
+ *             token are -1; a request without tokens gets GDR_SLOT_SKIP.
+ *
+ * A request is skipped (src GDR_SLOT_SKIP, dst -1, its tokens still counted)
+ * and GDR_ERR_SLOT recorded in the device status word if its kept count is
+ * not in [0, W], it needs more slots than W, a slot it needs is not in
+ * [0, slots), or its tokens do not end within max_tokens (offsets are clamped
+ * to max_tokens); a negative length counts as 0 and is recorded too.
+ * R <= 65536; one launch, no workspace; outputs may not overlap inputs.
+ */
+gdr_status gdr_slot_map(const int *lens, const int *kept, const int *table,
+                        long long table_stride, int R, int W, int slots, int max_tokens,
+                        int keep_all, int *cu_seqlens, int *request, int *src, int *dst,
+                        gdr_stream_t stream);
+
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 } gdr_act;
+
+/*
+ * The mixer's output norm: group norm, channels last, with an activation.
+ * The channels of a token fall into G groups of D (the heads of o); each
+ * group of each token is normalised by its own mean square (or, with center,
+ * its own mean and variance), so nothing is mixed over time:
+ *
+ *   n = (x - m) / sqrt(mean((x - m)^2) + eps),   m = center ? mean(x) : 0
+ *   l = n w + b
+ *   y = act(z) l   with a gate z,   y = act(l)   without (z NULL)
+ *
+ *   x      [rows, G, D] dtype    rows x_stride elements apart
+ *   z      [rows, G, D] dtype or NULL, rows z_stride elements apart
+ *   weight, bias  fp32 or NULL (1 / 0): [G, D] if per_channel, else [D]
+ *   y      [rows, G, D] dtype    dense
+ *
+ * 1 <= D <= 1024, G * D <= 65536.  Pointers aligned to their element; calls
+ * whose pointers, strides and D are multiples of 16 bytes run fastest.  y may
+ * be x (dense).  fp32 statistics; one launch, no workspace.
+ */
+gdr_status gdr_group_norm_fwd(const void *x, const void *z, gdr_dtype dtype, long long x_stride,
+                              long long z_stride, const float *weight, const float *bias,
+                              int per_channel, gdr_act act, int center, float eps, void *y,
+                              long long rows, int G, int D, gdr_stream_t stream);
+
+/*
+ * Gradients of gdr_group_norm_fwd from dy = dL/dy [rows, G, D] dtype (dense):
+ *
+ *   dx       [rows, G, D] fp32 (dense): what gdr_chunk_bwd reads as dout
+ *   dz       [rows, G, D] dtype (dense), or NULL: not written
+ *   dweight, dbias  fp32, shaped as weight and bias, or NULL
+ *
+ * The statistics are computed again from x.  Sums over rows run in a fixed
+ * order (the same call gives the same bits).  dweight / dbias need
+ * gdr_group_norm_bwd_workspace_bytes of workspace (16-byte aligned; calls
+ * that overlap on the GPU need one each); two launches with them, else one.
+ * dz needs z.
+ */
+size_t gdr_group_norm_bwd_workspace_bytes(long long rows, int G, int D, gdr_dtype dtype,
+                                          int per_channel);
+gdr_status gdr_group_norm_bwd(const void *dy, const void *x, const void *z, gdr_dtype dtype,
+                              long long x_stride, long long z_stride, const float *weight,
+                              const float *bias, int per_channel, gdr_act act, int center,
+                              float eps, float *dx, void *dz, float *dweight, float *dbias,
+                              long long rows, int G, int D, void *workspace, size_t ws_bytes,
+                              gdr_stream_t stream);
+
+/*
+ * The prologue of gdr_chunk_fwd_prologue as a map of its own (training keeps
+ * its outputs for the backward), with q and k heads shared by several value
+ * heads: value head h takes key head h / (H / Hk).
+ *
+ *   q, k   [tokens, Hk, dk] in_dtype  raw projections, rows q_stride /
+ *                                     k_stride elements apart
+ *   a      [tokens, H] or [tokens, H, dk] fp32; b [tokens, H] fp32 logits
+ *   gate_scale [H] fp32, > 0
+ *   qn, kn [tokens, H, dk] in_dtype (dense): q, k (normalised per norm_qk),
+ *                                     one copy for each value head
+ *   g      as a: -gate_scale[h] softplus(a);  beta [tokens, H]: sigmoid(b)
+ *
+ * qn, kn, g, beta are the inputs of gdr_chunk_fwd and gdr_chunk_bwd (with
+ * tokens = B * T).  dk in {32, 64, 128}, H a multiple of Hk, pointers 16-byte
+ * aligned, strides multiples of 16 bytes.  One launch, no workspace.
+ */
+gdr_status gdr_prologue_fwd(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
+                            long long k_stride, const float *a, gdr_gate_kind gate,
+                            const float *b, const float *gate_scale, int norm_qk, void *qn,
+                            void *kn, float *g, float *beta, long long tokens, int Hk, int H,
+                            int dk, gdr_stream_t stream);
+
+/*
+ * Gradients of gdr_prologue_fwd from those of its outputs (all dense fp32, as
+ * gdr_chunk_bwd writes them): dqn, dkn [tokens, H, dk], dg as a, dbeta
+ * [tokens, H].
+ *
+ *   dq, dk_  [tokens, Hk, dk] in_dtype (dense): summed over the value heads
+ *            that share a key head, then through the normalisation
+ *   da       as a, fp32;  db [tokens, H] fp32
+ *   dgate_scale [H] fp32, summed over tokens in a fixed order
+ *
+ * The rounding of qn, kn to in_dtype counts as the identity.  Needs
+ * gdr_prologue_bwd_workspace_bytes of workspace (16-byte aligned; calls that
+ * overlap on the GPU need one each); two launches.
+ */
+size_t gdr_prologue_bwd_workspace_bytes(long long tokens, int H, int dk, gdr_gate_kind gate);
+gdr_status gdr_prologue_bwd(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
+                            long long k_stride, const float *a, gdr_gate_kind gate,
+                            const float *b, const float *gate_scale, int norm_qk,
+                            const float *dqn, const float *dkn, const float *dg,
+                            const float *dbeta, void *dq, void *dk_, float *da, float *db,
+                            float *dgate_scale, long long tokens, int Hk, int H, int dk,
+                            void *workspace, size_t ws_bytes, gdr_stream_t stream);
+
 /*
  * Synchronises `stream`, then reads and clears the device status word.
  * Returns GDR_OK, GDR_ERR_TIMEOUT (a kernel gave up a bounded wait since the
  * last call), GDR_ERR_RANGE (a per-channel gate decayed beyond the
- * tensor-core path's range in some chunk since the last call; a time-out
- * takes precedence when both happened) or GDR_ERR_CUDA (the
- * synchronisation itself failed).
+ * tensor-core path's range in some chunk since the last call), GDR_ERR_SLOT
+ * (a request of gdr_slot_map or gdr_step_slots named what does not exist
+ * since the last call; of several the first in this order is returned) or
+ * GDR_ERR_CUDA (the synchronisation itself failed).
  */
 gdr_status gdr_get_device_status(gdr_stream_t stream);
 
