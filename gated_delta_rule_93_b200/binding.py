@@ -2,13 +2,16 @@
 
 Every step of the computation runs in the library's CUDA kernels; this
 module checks tensor devices, dtypes, shapes and contiguity, then passes
-raw device pointers and the current CUDA stream through ctypes.  There is no
+raw device pointers and the current CUDA stream through ctypes (the operators
+around the mixer through a compiled front end, at the end).  There is no
 CPU fallback: if the library is missing, or a tensor is not on a CUDA
 device, the call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -16,7 +19,9 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
+NATIVE_PATH = os.path.join(_HERE, "_gdr_torch.so")
 _lib = None
+_native = None
 _lock = threading.Lock()
 
 GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_WORKSPACE, GDR_ERR_CUDA, \
@@ -574,83 +579,36 @@ def dplr_fwd(q, k, v, a, b, g, S0=None, *, output_final_state=True, o=None, S_T=
 
 # ------------------------------------------------------------------------------
 # The operators around the mixer.  A decode loop calls them once per layer and
-# token, so their checks cost as little as they can: `_expect` looks at a
-# tensor once and leaves the wording of an error to `_need`.
+# token, so their checks and marshalling are compiled (csrc/gdr_torch.cpp); the
+# functions here name and document the arguments.
 
-def _expect(t, name, dtype, shape, device):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_contiguous()):
-        _need(t, name, dtype, shape, device)
-
-
-def _row_stride(t, name, dtype, shape, device):
-    """Elements between the rows of ``t`` [..., H, d]: the last two dimensions
-    are dense, those before them advance by one distance (a slice of a fused
-    projection, for example)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (no CPU path exists)")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return shape[-1] * shape[-2]
-    size, stride = t.shape, t.stride()
-    width, row = size[-1] * size[-2], None
-    ok = (size[-1] == 1 or stride[-1] == 1) and (size[-2] == 1 or stride[-2] == size[-1])
-    count = 1  # rows covered by the dimensions from the last leading one on
-    for n, step in zip(reversed(size[:-2]), reversed(stride[:-2])):
-        if n == 1:
-            continue
-        if row is None:
-            row = step
-        ok = ok and step == row * count
-        count *= n
-    if not ok or (row is not None and row < width):
-        raise ValueError(f"{name} must have dense last two dimensions and rows one distance apart "
-                         f"(strides {tuple(stride)} of shape {tuple(size)})")
-    return width if row is None else row
+def native():
+    """Load the compiled front end once, with the library behind it."""
+    global _native
+    L = lib()
+    with _lock:
+        if _native is None:
+            if not os.path.exists(NATIVE_PATH):
+                raise RuntimeError(
+                    f"{NATIVE_PATH} is missing: build it with "
+                    "`python -m gated_delta_rule_93_b200.build` (no CPU fallback exists)")
+            loader = importlib.machinery.ExtensionFileLoader("_gdr_torch", NATIVE_PATH)
+            spec = importlib.util.spec_from_file_location("_gdr_torch", NATIVE_PATH, loader=loader)
+            mod = importlib.util.module_from_spec(spec)
+            loader.exec_module(mod)
+            mod.connect(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+                "gdr_step_slots", "gdr_slot_map", "gdr_group_norm_fwd", "gdr_group_norm_bwd",
+                "gdr_group_norm_bwd_workspace_bytes", "gdr_prologue_fwd", "gdr_prologue_bwd",
+                "gdr_prologue_bwd_workspace_bytes")))
+            _native = mod
+    return _native
 
 
-def _launch(fn, device, stream, *args):
-    """Call ``fn(*args, stream)`` with ``device`` current."""
-    index = device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        if stream.device.index != index:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, handle)
-    if rc:
-        _check(rc)
-
-
-def _owned_by(stream, *tensors):
-    """Keep what this module allocated for a call on ``stream`` until it is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None and t.numel():
-                t.record_stream(stream)
-
-
-def _workspace(workspace, need, device, stream):
-    """The caller's workspace, looked at, or a new one of ``need`` bytes."""
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        _owned_by(stream, workspace)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or \
-            not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace
+def _act(name):
+    try:
+        return GDR_ACTS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"act must be one of {', '.join(GDR_ACTS)}, got {name!r}") from None
 
 
 def step_slots(q, k, v, g, beta, pool, src, *, dst=None, cu_seqlens=None, gate_scale=None,
@@ -666,51 +624,11 @@ def step_slots(q, k, v, g, beta, pool, src, *, dst=None, cu_seqlens=None, gate_s
     dst a request's last state goes back to src.  Rows of ``o`` that no request
     covers are left as they were (unset in an ``o`` allocated here).
     """
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [total, Hk, dk] tensor")
-    dev, dt = q.device, q.dtype
-    total, Hk, dk = q.shape
-    if not isinstance(v, torch.Tensor) or v.dim() != 3:
-        raise ValueError("v must be a [total, H, dv] tensor")
-    H, dv = v.shape[1:]
-    qs = _row_stride(q, "q", dt, (total, Hk, dk), dev)
-    ks = _row_stride(k, "k", dt, (total, Hk, dk), dev)
-    vs = _row_stride(v, "v", dt, (total, H, dv), dev)
-    gk = GDR_GATE_PER_CHANNEL if g.dim() == 3 else GDR_GATE_SCALAR
-    f32, i32 = torch.float32, torch.int32
-    _expect(g, "g", f32, (total, H, dk) if gk else (total, H), dev)
-    _expect(beta, "beta", f32, (total, H), dev)
-    if gate_scale is not None:
-        _expect(gate_scale, "gate_scale", f32, (H,), dev)
-    slots = pool.shape[0]
-    if pool.is_contiguous():
-        _expect(pool, "pool", f32, (slots, H, dv, dk), dev)
-        slot_stride = H * dv * dk
-    else:
-        if pool.dim() != 4 or pool.stride()[1:] != (dv * dk, dk, 1):
-            raise ValueError("the slots of pool [slots, H, dv, dk] must be dense")
-        slot_stride = _row_stride(pool.flatten(2), "pool", f32, (slots, H, dv * dk), dev)
-    R = src.shape[0] if src.dim() == 1 else -1
-    _expect(src, "src", i32, (max(R, 0),), dev)
-    if dst is not None:
-        _expect(dst, "dst", i32, (total,), dev)
-    if cu_seqlens is not None:
-        _expect(cu_seqlens, "cu_seqlens", i32, (R + 1,), dev)
-    elif R != total:
-        raise ValueError(f"without cu_seqlens src must hold one slot for each of {total} tokens")
-    if o is None:
-        o = torch.empty((total, H, dv), dtype=dt, device=dev)
-        _owned_by(stream, o)
-    else:
-        _expect(o, "o", dt, (total, H, dv), dev)
-    _launch((_lib or lib()).gdr_step_slots, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            _in_dtype(dt), qs, ks, vs, g.data_ptr(), gk, beta.data_ptr(),
-            None if gate_scale is None else gate_scale.data_ptr(),
-            (1 if norm_q else 0) | (2 if norm_k else 0), pool.data_ptr(), slots, slot_stride,
-            src.data_ptr(), None if dst is None else dst.data_ptr(),
-            None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(), R, total, Hk, H,
-            dk, dv)
-    return o
+    r = (_native or native()).step_slots(q, k, v, g, beta, pool, src, dst, cu_seqlens, gate_scale,
+                                         norm_q, norm_k, o, stream)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def slot_map(lens, kept, table, slots, max_tokens, *, keep_all=True, out=None, stream=None):
@@ -719,59 +637,13 @@ def slot_map(lens, kept, table, slots, max_tokens, *, keep_all=True, out=None, s
     lens, kept [R] and table [R,W] int32 (rows any distance apart); ``slots``
     is the size of the pool, ``max_tokens`` the room for tokens.  Returns a
     dict of int32 tensors: cu_seqlens [R+1], src [R], request and dst
-    [max_tokens] (see ``step_slots``; -1 behind the last token).
+    [max_tokens] (see ``step_slots``; -1 behind the last token), pieces of one
+    allocation unless ``out`` is such a dict.
     """
-    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
-        raise ValueError("lens must be a [R] tensor")
-    if not lens.is_cuda:
-        raise ValueError("lens must be on a CUDA device (no CPU path exists)")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a [R, W] tensor")
-    dev, i32 = lens.device, torch.int32
-    R, W = table.shape
-    _expect(lens, "lens", i32, (R,), dev)
-    _expect(kept, "kept", i32, (R,), dev)
-    ts = W
-    if table.is_contiguous():
-        _expect(table, "table", i32, (R, W), dev)
-    else:
-        ts = _row_stride(table[:, None], "table", i32, (R, 1, W), dev)
-    if out is None:
-        room = max(max_tokens, 0)
-        parts = torch.empty(2 * R + 1 + 2 * room, dtype=i32, device=dev)
-        _owned_by(stream, parts)
-        cu, src, request, dst = parts.split((R + 1, R, room, room))
-        out = {"cu_seqlens": cu, "src": src, "request": request, "dst": dst}
-    else:
-        for name, n in (("cu_seqlens", R + 1), ("src", R), ("request", max_tokens),
-                        ("dst", max_tokens)):
-            _expect(out[name], name, i32, (n,), dev)
-    _launch((_lib or lib()).gdr_slot_map, dev, stream, lens.data_ptr(), kept.data_ptr(),
-            table.data_ptr(), ts, R, W, slots, max_tokens, 1 if keep_all else 0,
-            out["cu_seqlens"].data_ptr(), out["request"].data_ptr(), out["src"].data_ptr(),
-            out["dst"].data_ptr())
-    return out
-
-
-def _norm_args(x, z, weight, bias, act):
-    """The checks both directions of the output norm share."""
-    if not isinstance(x, torch.Tensor) or x.dim() < 2:
-        raise ValueError("x must be a [..., G, D] tensor")
-    dev, dt, shape = x.device, x.dtype, x.shape
-    G, D = shape[-2:]
-    xs = _row_stride(x, "x", dt, shape, dev)
-    zs = _row_stride(z, "z", dt, shape, dev) if z is not None else 0
-    per = weight if weight is not None else bias
-    per_channel = per is not None and per.dim() == 2
-    affine = (G, D) if per_channel else (D,)
-    if weight is not None:
-        _expect(weight, "weight", torch.float32, affine, dev)
-    if bias is not None:
-        _expect(bias, "bias", torch.float32, affine, dev)
-    if act not in GDR_ACTS:
-        raise ValueError(f"act must be one of {', '.join(GDR_ACTS)}, got {act!r}")
-    rows = x.numel() // (G * D) if G * D else 0
-    return dev, dt, shape, rows, G, D, xs, zs, 1 if per_channel else 0, affine
+    r = (_native or native()).slot_map(lens, kept, table, slots, max_tokens, keep_all, out, stream)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def group_norm_fwd(x, z=None, weight=None, bias=None, *, act="silu", center=False, eps=1e-5,
@@ -780,21 +652,13 @@ def group_norm_fwd(x, z=None, weight=None, bias=None, *, act="silu", center=Fals
     an activation.  Returns y, shaped as x.
 
     x [..., G, D] and the gate z (or None) bf16 or fp32, rows any distance
-    apart; weight, bias fp32 [D] or [G, D] or None.  y = act(z) l or, without
-    z, act(l), where l = n w + b.
+    apart; weight, bias fp32 [D] or [G, D] or None; act "silu", "sigmoid" or
+    "none".  y = act(z) l or, without z, act(l), where l = n w + b.
     """
-    dev, dt, shape, rows, G, D, xs, zs, pc, _ = _norm_args(x, z, weight, bias, act)
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
-        _owned_by(stream, y)
-    else:
-        _expect(y, "y", dt, shape, dev)
-    _launch((_lib or lib()).gdr_group_norm_fwd, dev, stream, x.data_ptr(),
-            None if z is None else z.data_ptr(), _in_dtype(dt), xs, zs,
-            None if weight is None else weight.data_ptr(),
-            None if bias is None else bias.data_ptr(), pc, GDR_ACTS[act], 1 if center else 0, eps,
-            y.data_ptr(), rows, G, D)
-    return y
+    r = (_native or native()).group_norm_fwd(x, z, weight, bias, _act(act), center, eps, y, stream)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def group_norm_bwd(dy, x, z=None, weight=None, bias=None, *, act="silu", center=False, eps=1e-5,
@@ -803,50 +667,14 @@ def group_norm_bwd(dy, x, z=None, weight=None, bias=None, *, act="silu", center=
 
     dy as x, contiguous.  Returns dict dx (fp32, what ``chunk_bwd`` takes as
     dout), dz (dtype of z), dweight, dbias (fp32); what has no input is None.
+    ``out`` may be such a dict, preallocated; ``workspace`` a CUDA tensor of
+    ``gdr_group_norm_bwd_workspace_bytes`` (calls that overlap need one each).
     """
-    dev, dt, shape, rows, G, D, xs, zs, pc, affine = _norm_args(x, z, weight, bias, act)
-    _expect(dy, "dy", dt, shape, dev)
-    f32 = torch.float32
-    want = {"dx": (f32, shape), "dz": (dt, shape) if z is not None else None,
-            "dweight": (f32, affine) if weight is not None else None,
-            "dbias": (f32, affine) if bias is not None else None}
-    if out is None:
-        out = {n: w and torch.empty(w[1], dtype=w[0], device=dev) for n, w in want.items()}
-        _owned_by(stream, *out.values())
-    else:  # (the caller's preallocated dict of the same tensors)
-        for n, w in want.items():
-            if w is not None:
-                _expect(out[n], n, w[0], w[1], dev)
-    L = _lib or lib()
-    if weight is not None or bias is not None:
-        need = L.gdr_group_norm_bwd_workspace_bytes(rows, G, D, _in_dtype(dt), pc)
-        workspace = _workspace(workspace, need, dev, stream)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _launch(L.gdr_group_norm_bwd, dev, stream, dy.data_ptr(), x.data_ptr(), ptr(z), _in_dtype(dt),
-            xs, zs, ptr(weight), ptr(bias), pc, GDR_ACTS[act], 1 if center else 0, eps,
-            out["dx"].data_ptr(), ptr(out["dz"]) if z is not None else None,
-            ptr(out["dweight"]) if weight is not None else None,
-            ptr(out["dbias"]) if bias is not None else None, rows, G, D, ptr(workspace),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    return out
-
-
-def _prologue_args(q, k, a, b, gate_scale):
-    """The checks both directions of the prologue share."""
-    if not isinstance(q, torch.Tensor) or q.dim() < 3:
-        raise ValueError("q must be a [..., Hk, dk] tensor")
-    dev, dt, shape = q.device, q.dtype, q.shape
-    lead, Hk, dk = shape[:-2], shape[-2], shape[-1]
-    qs = _row_stride(q, "q", dt, shape, dev)
-    ks = _row_stride(k, "k", dt, shape, dev)
-    H = b.shape[-1]
-    gk = GDR_GATE_PER_CHANNEL if a.dim() == q.dim() else GDR_GATE_SCALAR
-    f32 = torch.float32
-    _expect(a, "a", f32, (*lead, H, dk) if gk else (*lead, H), dev)
-    _expect(b, "b", f32, (*lead, H), dev)
-    _expect(gate_scale, "gate_scale", f32, (H,), dev)
-    tokens = b.numel() // H if H else 0
-    return dev, dt, shape, (*lead, H, dk), tokens, Hk, H, dk, qs, ks, gk
+    r = (_native or native()).group_norm_bwd(x, z, weight, bias, _act(act), center, eps, dy,
+                                             workspace, out, stream)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def prologue_fwd(q, k, a, b, gate_scale, *, norm_q=True, norm_k=True, out=None, stream=None):
@@ -856,25 +684,13 @@ def prologue_fwd(q, k, a, b, gate_scale, *, norm_q=True, norm_k=True, out=None, 
     q, k [..., Hk, dk] raw (bf16 or fp32, rows any distance apart); a [..., H]
     or [..., H, dk] and b [..., H] fp32 logits; gate_scale [H] fp32.  q, k come
     back normalised (per the flags) with one copy for each of the H value
-    heads; g = -gate_scale softplus(a), beta = sigmoid(b).
+    heads; g = -gate_scale softplus(a), beta = sigmoid(b).  ``out`` may be the
+    preallocated tuple of them.
     """
-    dev, dt, _, full, tokens, Hk, H, dk, qs, ks, gk = _prologue_args(q, k, a, b, gate_scale)
-    if out is None:
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-        out = (new(full, dt), new(full, dt), new(a.shape, torch.float32),
-               new(b.shape, torch.float32))
-        _owned_by(stream, *out)
-    else:  # (the caller's preallocated q, k, g, beta)
-        for t, n, d, s in zip(out, ("q out", "k out", "g", "beta"),
-                              (dt, dt, torch.float32, torch.float32),
-                              (full, full, a.shape, b.shape)):
-            _expect(t, n, d, s, dev)
-    qn, kn, g, beta = out
-    _launch((_lib or lib()).gdr_prologue_fwd, dev, stream, q.data_ptr(), k.data_ptr(),
-            _in_dtype(dt), qs, ks, a.data_ptr(), gk, b.data_ptr(), gate_scale.data_ptr(),
-            (1 if norm_q else 0) | (2 if norm_k else 0), qn.data_ptr(), kn.data_ptr(),
-            g.data_ptr(), beta.data_ptr(), tokens, Hk, H, dk)
-    return qn, kn, g, beta
+    r = (_native or native()).prologue_fwd(q, k, a, b, gate_scale, norm_q, norm_k, out, stream)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def prologue_bwd(q, k, a, b, gate_scale, dq, dk, dg, dbeta, *, norm_q=True, norm_k=True,
@@ -883,29 +699,11 @@ def prologue_bwd(q, k, a, b, gate_scale, dq, dk, dg, dbeta, *, norm_q=True, norm
     those of its outputs, as ``chunk_bwd`` returns them (fp32).
 
     dq, dk [..., H, dk]; dg as a; dbeta [..., H].  Returns dict dq, dk (shape
-    and dtype of the raw q, k), da, db, dgate_scale (fp32).
+    and dtype of the raw q, k), da, db, dgate_scale (fp32).  ``out`` and
+    ``workspace`` as in ``group_norm_bwd``.
     """
-    dev, dt, shape, full, tokens, Hk, H, d, qs, ks, gk = _prologue_args(q, k, a, b, gate_scale)
-    f32 = torch.float32
-    _expect(dq, "dq", f32, full, dev)
-    _expect(dk, "dk", f32, full, dev)
-    _expect(dg, "dg", f32, a.shape, dev)
-    _expect(dbeta, "dbeta", f32, b.shape, dev)
-    want = {"dq": (dt, shape), "dk": (dt, shape), "da": (f32, a.shape), "db": (f32, b.shape),
-            "dgate_scale": (f32, (H,))}
-    if out is None:
-        out = {n: torch.empty(s, dtype=t, device=dev) for n, (t, s) in want.items()}
-        _owned_by(stream, *out.values())
-    else:  # (the caller's preallocated dict of the same tensors)
-        for n, (t, s) in want.items():
-            _expect(out[n], n, t, s, dev)
-    L = _lib or lib()
-    workspace = _workspace(workspace, L.gdr_prologue_bwd_workspace_bytes(tokens, H, d, gk), dev,
-                           stream)
-    _launch(L.gdr_prologue_bwd, dev, stream, q.data_ptr(), k.data_ptr(), _in_dtype(dt), qs, ks,
-            a.data_ptr(), gk, b.data_ptr(), gate_scale.data_ptr(),
-            (1 if norm_q else 0) | (2 if norm_k else 0), dq.data_ptr(), dk.data_ptr(),
-            dg.data_ptr(), dbeta.data_ptr(), out["dq"].data_ptr(), out["dk"].data_ptr(),
-            out["da"].data_ptr(), out["db"].data_ptr(), out["dgate_scale"].data_ptr(), tokens, Hk,
-            H, d, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return out
+    r = (_native or native()).prologue_bwd(q, k, a, b, gate_scale, norm_q, norm_k, dq, dk, dg,
+                                           dbeta, workspace, out, stream)
+    if type(r) is int:
+        _check(r)
+    return r

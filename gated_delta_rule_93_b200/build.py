@@ -1,10 +1,12 @@
-"""Build ``libgdr.so`` (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build ``libgdr.so`` (the C-ABI library) in-tree with nvcc for sm_100a, and
+``_gdr_torch.so`` (the compiled torch front end of some of its entry points).
 
 Usage: ``python -m gated_delta_rule_93_b200.build [--force] [-v]``.
 Each ``csrc/*.cu`` compiles to ``_build/*.o`` in parallel (skipped when the
 object is newer than its inputs), then nvcc links the shared library with
 the CUDA runtime linked statically, so the library loads on a machine with
-no GPU driver (only the first CUDA call needs one).
+no GPU driver (only the first CUDA call needs one).  The front end is host
+code, compiled with g++ against the installed torch.
 """
 from __future__ import annotations
 
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr.so")
+NATIVE = os.path.join(PKG, "_gdr_torch.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -48,6 +52,28 @@ def _compile(src, verbose):
     return obj, r.stderr
 
 
+def _compile_native(src):
+    """The torch front end: g++, linked to the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(),
+           os.path.join(cuda, "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + ".tmp%d" % os.getpid()
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{p}" for p in inc), src, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {src}:\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -55,10 +81,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     todo = [s for s in srcs
             if force or _stale(os.path.join(BUILD, os.path.basename(s)[:-3] + ".o"), [s] + deps)]
     logs = []
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as ex:
+    front = os.path.join(CSRC, "gdr_torch.cpp")
+    front_stale = force or _stale(NATIVE, [front] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if todo or front_stale:
+        workers = max(1, min(len(todo) + 1, os.cpu_count() or 1))
+        with cf.ThreadPoolExecutor(max_workers=workers) as ex:
+            front_done = ex.submit(_compile_native, front) if front_stale else None
             for obj, log in ex.map(lambda s: _compile(s, verbose), todo):
                 logs.append(log)
+            if front_done:
+                front_done.result()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     if force or todo or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()

@@ -135,18 +135,25 @@ def test_cpu_tensors_are_refused(L):
     ((512, 64, 1), (5, 8, 64), 512), ((800, 64, 1), (5, 8, 64), 800),
     ((4800, 800, 64, 1), (3, 6, 8, 64), 800), ((64, 64, 1), (1, 8, 64), 512),
     ((9999, 800, 64, 1), (1, 6, 8, 64), 800), ((300, 7, 1), (5, 1, 64), 300)])
-def test_row_stride(monkeypatch, stride, shape, row):
-    buf = torch.zeros(60000)
-    t = buf.as_strided(shape, stride)
-    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
-    assert binding._row_stride(t, "t", torch.float32, t.shape, t.device) == row
+def test_rows_apart(L, stride, shape, row):
+    assert binding.native().rows_apart(torch.zeros(60000).as_strided(shape, stride), "t") == row
 
 
 @pytest.mark.parametrize("stride,shape", [
     ((512, 65, 1), (5, 8, 64)), ((1024, 128, 2), (5, 8, 64)), ((5000, 800, 64, 1), (3, 6, 8, 64)),
     ((0, 64, 1), (5, 8, 64)), ((64, 512, 1), (8, 5, 64)), ((100, 64, 1), (5, 8, 64))])
-def test_row_stride_refuses(monkeypatch, stride, shape):
-    t = torch.zeros(60000).as_strided(shape, stride)
-    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+def test_rows_apart_refuses(L, stride, shape):
     with pytest.raises(ValueError, match="rows one distance apart"):
-        binding._row_stride(t, "t", torch.float32, t.shape, t.device)
+        binding.native().rows_apart(torch.zeros(60000).as_strided(shape, stride), "t")
+
+
+def test_front_end_refuses_what_is_not_a_tensor(L):
+    x = torch.zeros(4, 2, 64)
+    with pytest.raises(TypeError, match="x must be a torch.Tensor"):
+        binding.group_norm_fwd([1.0])
+    with pytest.raises(ValueError, match="act must be one of"):
+        binding.group_norm_fwd(x, act="gelu")
+    with pytest.raises(ValueError, match="act must be one of"):
+        binding.group_norm_fwd(x, act=[])
+    with pytest.raises(TypeError, match="expected 9 arguments"):
+        binding.native().group_norm_fwd(x)
