@@ -1,0 +1,72 @@
+// The mixer's output norm: group norm, channels last, with an activation.
+// What its two directions share.
+//
+// A group (one head of one token) is a few hundred bytes, so L lanes of a
+// warp hold it in registers: every input is read once, every sum over the
+// group is a few shuffles, every output is written once.  Both directions are
+// bound by HBM as long as enough bytes are in flight: U rows of a lane are
+// requested before the first of them is used.
+//
+// A lane keeps the same group index for all its rows (the number of groups
+// in flight is a multiple of G), so its weights are loaded once.
+#pragma once
+
+#include "gdr_rows.cuh"
+
+namespace gdr {
+
+inline bool multiple_of(const void *p, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+// Elements per access: 16 bytes where every row and group starts on 16; for
+// bf16 also pairs; else single elements.
+inline int norm_vector(const GroupNormArgs &a) {
+  const int size = a.bf16 ? 2 : 4;
+  for (int vec : {16 / size, 2}) {
+    if (vec == 2 && !a.bf16) break;
+    const size_t bytes = (size_t)vec * size, wide = bytes < 8 ? 8 : 16;  // wide: of fp32 outputs
+    if (a.D % vec == 0 && a.x_stride % vec == 0 && (!a.z || a.z_stride % vec == 0) &&
+        multiple_of(a.x, bytes) && multiple_of(a.z, bytes) && multiple_of(a.dy, bytes) &&
+        multiple_of(a.y, bytes) && multiple_of(a.dz, bytes) && multiple_of(a.dx, wide))
+      return vec;
+  }
+  return 1;
+}
+
+// Calls f.template operator()<T, VEC, L, NV>() for the layout of these
+// arguments: L lanes a group, NV accesses of VEC elements a lane.
+template <typename T, int VEC, typename F>
+cudaError_t norm_layout_vec(int D, F f) {
+  const int n = (D + VEC - 1) / VEC;  // accesses of a group
+  if constexpr (sizeof(T) * VEC == 16) {
+    if (n <= 4) return f.template operator()<T, VEC, 4, 1>();
+    if (n <= 8) return f.template operator()<T, VEC, 8, 1>();
+    if (n <= 16) return f.template operator()<T, VEC, 16, 1>();
+  }
+  if (n <= 32) return f.template operator()<T, VEC, 32, 1>();
+  if (n <= 64) return f.template operator()<T, VEC, 32, 2>();
+  if (n <= 128) return f.template operator()<T, VEC, 32, 4>();
+  if constexpr (VEC <= 4) {
+    if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
+  }
+  if constexpr (VEC <= 2) {
+    if (n <= 512) return f.template operator()<T, VEC, 32, 16>();
+  }
+  if constexpr (VEC == 1) {
+    if (n <= 1024) return f.template operator()<T, VEC, 32, 32>();
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename F>
+cudaError_t norm_layout(const GroupNormArgs &a, F f) {
+  const int vec = norm_vector(a);
+  if (!a.bf16)
+    return vec == 4 ? norm_layout_vec<float, 4>(a.D, f) : norm_layout_vec<float, 1>(a.D, f);
+  if (vec == 8) return norm_layout_vec<__nv_bfloat16, 8>(a.D, f);
+  return vec == 2 ? norm_layout_vec<__nv_bfloat16, 2>(a.D, f)
+                  : norm_layout_vec<__nv_bfloat16, 1>(a.D, f);
+}
+
+}  // namespace gdr

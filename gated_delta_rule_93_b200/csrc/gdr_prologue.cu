@@ -8,179 +8,189 @@
 //   ds_h = -sum dg softplus(a)
 //
 // L lanes hold one key head of one token in registers (16-byte accesses), so
-// every tensor is read once and written once: bound by HBM.  The gates are
-// elementwise work of other blocks of the same launch.  The gate threads of
-// the backward keep one head for all their tokens (their number is a multiple of H), so ds adds
-// up in registers; a second launch adds their partial sums in a fixed order.
+// every tensor is read once and written once: bound by HBM, with the loads of
+// U tokens of q and k requested before the first is used.  The gates are the work
+// of other blocks of the same launch: a thread for a (token, head) with a
+// scalar gate, dk / 4 lanes with a per-channel one.  Every slot keeps its head
+// for all its tokens (no division in the loops), so ds adds up in registers;
+// a second launch adds the slots' sums in a fixed order.
 #include "gdr_rows.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr float kNormEps = 1e-6f;
+constexpr int kMaxBlocks = 4 * kSMs;  // of each kind of work
 
-// Blocks of the two kinds of work, and the gate slots (backward).
 struct Split {
-  int norm_blocks, gate_blocks;
-  int slots;       // gate slots in use (a multiple of H)
-  long long step;  // tokens between a slot's gates
+  RowPlan norm, gate;
 };
 
-int blocks_for(long long items, int per_block) {
-  const long long n = (items + per_block - 1) / per_block;
-  return (int)(n < 1 ? 1 : n > kRowBlocks ? kRowBlocks : n);
+Split make_split(const PrologueArgs &a, int L) {
+  const int lanes = a.per_channel ? a.d / 4 : 1;
+  return {row_plan(a.tokens, a.Hk, kRowThreads / L, kMaxBlocks),
+          row_plan(a.tokens, a.H, kRowThreads / lanes, kMaxBlocks)};
 }
 
-// Gate slots: a thread for a (token, head) with a scalar gate, dk / 4 lanes
-// with a per-channel one.
-Split make_split(long long tokens, int H, int dk, int per_channel) {
-  Split s;
-  const int per_block = kRowThreads / (per_channel ? dk / 4 : 1);
-  s.norm_blocks = 0;
-  s.gate_blocks = blocks_for(tokens * H, per_block);
-  const int least = (H + per_block - 1) / per_block;  // every head once
-  if (s.gate_blocks < least) s.gate_blocks = least;
-  s.step = (long long)s.gate_blocks * per_block / H;
-  s.slots = (int)(s.step * H);
-  return s;
-}
-
-template <typename T, int VEC, int L>
-__global__ void __launch_bounds__(kRowThreads) prologue_fwd_kernel(PrologueArgs a, Split p) {
-  if ((int)blockIdx.x >= p.norm_blocks) {
-    const long long step = (long long)p.gate_blocks * kRowThreads;
-    const long long first = (long long)(blockIdx.x - p.norm_blocks) * kRowThreads + threadIdx.x;
-    for (long long i = first; i < a.tokens * a.H; i += step) {
-      a.beta[i] = sigmoid(a.b[i]);
-      if (!a.per_channel) a.g[i] = -a.gate_scale[i % a.H] * softplus(a.a[i]);
-    }
-    if (a.per_channel) {
-      const int quads = a.d / 4;
-      for (long long i = first; i < a.tokens * a.H * quads; i += step) {
-        float x[4];
-        load_vec<float, 4>(a.a + 4 * i, x);
-        const float s = -a.gate_scale[(i / quads) % a.H];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = s * softplus(x[e]);
-        store_vec<float, 4>(a.g + 4 * i, x);
-      }
-    }
-    return;
-  }
-  const int lane = threadIdx.x % L;
-  const int share = a.H / a.Hk;
-  const long long groups = a.tokens * a.Hk;
-  const long long step = (long long)p.norm_blocks * (kRowThreads / L);
-  const long long turns = (groups + step - 1) / step;
-  long long f = (long long)blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
-  for (long long k = 0; k < turns; ++k, f += step) {
-    const bool live = f < groups;
-    const long long t = f / a.Hk;
-    const int hk = (int)(f % a.Hk);
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const T *in = static_cast<const T *>(which ? a.k : a.q) +
-                    t * (which ? a.k_stride : a.q_stride) + hk * a.d + lane * VEC;
-      float x[VEC] = {};
-      if (live) load_vec<T, VEC>(in, x);
-      if (a.norm_qk & (which ? GDR_NORM_K : GDR_NORM_Q)) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) ss += x[e] * x[e];
-        const float r = rsqrtf(lanes_sum<L>(ss) + kNormEps);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] *= r;
-      }
-      T *out = static_cast<T *>(which ? a.kn : a.qn) + (t * a.H + hk * share) * a.d + lane * VEC;
-      if (live)
-        for (int s = 0; s < share; ++s) store_vec<T, VEC>(out + s * a.d, x);
-    }
-  }
-}
-
-template <typename T, int VEC, int L>
-__global__ void __launch_bounds__(kRowThreads) prologue_bwd_kernel(PrologueArgs a, Split p) {
-  if ((int)blockIdx.x >= p.norm_blocks) {
-    const int thread = (blockIdx.x - p.norm_blocks) * kRowThreads + threadIdx.x;
-    float ds = 0.f;
+// g and beta of one block's gate slots.
+__device__ __forceinline__ void gates_fwd(const PrologueArgs &a, const RowPlan &p, int block) {
+  const int thread = block * kRowThreads + threadIdx.x;
+  const int quads = a.per_channel ? a.d / 4 : 1, slot = thread / quads, lane = thread % quads;
+  if (slot >= p.slots) return;
+  const int h = slot % a.H;
+  const float s = -a.gate_scale[h];
+  for (long long t = slot / a.H; t < a.tokens; t += p.step) {
+    const long long th = t * a.H + h;
+    if (lane == 0) a.beta[th] = sigmoid(a.b[th]);
     if (!a.per_channel) {
-      if (thread >= p.slots) return;
-      const int h = thread % a.H;
-      const float s = a.gate_scale[h];
-      for (long long t = thread / a.H; t < a.tokens; t += p.step) {
-        const long long i = t * a.H + h;
-        const float x = a.a[i], dg = a.dg[i], beta = sigmoid(a.b[i]);
-        a.da[i] = -s * sigmoid(x) * dg;
-        a.db[i] = beta * (1.f - beta) * a.dbeta[i];
-        ds -= dg * softplus(x);
-      }
-      a.ws[thread] = ds;
+      a.g[th] = s * softplus(a.a[th]);
     } else {
-      const int quads = a.d / 4, slot = thread / quads, lane = thread % quads;
-      const bool used = slot < p.slots;
-      const int h = slot % a.H;
-      const float s = a.gate_scale[h];
-      if (used)
-        for (long long t = slot / a.H; t < a.tokens; t += p.step) {
-          const long long th = t * a.H + h, i = th * a.d + 4 * lane;
-          float x[4], dg[4];
-          load_vec<float, 4>(a.a + i, x);
-          load_vec<float, 4>(a.dg + i, dg);
+      float x[4];
+      load_vec<float, 4>(a.a + th * a.d + 4 * lane, x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ds -= dg[e] * softplus(x[e]);
-            x[e] = -s * sigmoid(x[e]) * dg[e];
-          }
-          store_vec<float, 4>(a.da + i, x);
-          if (lane == 0) {
-            const float beta = sigmoid(a.b[th]);
-            a.db[th] = beta * (1.f - beta) * a.dbeta[th];
-          }
-        }
-      for (int m = quads / 2; m; m >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, m);
-      if (used && lane == 0) a.ws[slot] = ds;
+      for (int e = 0; e < 4; ++e) x[e] = s * softplus(x[e]);
+      store_vec<float, 4>(a.g + th * a.d + 4 * lane, x);
     }
+  }
+}
+
+// da, db and the slot's part of ds.
+__device__ __forceinline__ void gates_bwd(const PrologueArgs &a, const RowPlan &p, int block) {
+  const int thread = block * kRowThreads + threadIdx.x;
+  const int quads = a.per_channel ? a.d / 4 : 1, slot = thread / quads, lane = thread % quads;
+  const bool used = slot < p.slots;
+  const int h = slot % a.H;
+  const float s = a.gate_scale[h];
+  float ds = 0.f;
+  if (used)
+    for (long long t = slot / a.H; t < a.tokens; t += p.step) {
+      const long long th = t * a.H + h;
+      if (lane == 0) {
+        const float beta = sigmoid(a.b[th]);
+        a.db[th] = beta * (1.f - beta) * a.dbeta[th];
+      }
+      if (!a.per_channel) {
+        const float x = a.a[th], dg = a.dg[th];
+        a.da[th] = -s * sigmoid(x) * dg;
+        ds -= dg * softplus(x);
+      } else {
+        float x[4], dg[4];
+        load_vec<float, 4>(a.a + th * a.d + 4 * lane, x);
+        load_vec<float, 4>(a.dg + th * a.d + 4 * lane, dg);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ds -= dg[e] * softplus(x[e]);
+          x[e] = -s * sigmoid(x[e]) * dg[e];
+        }
+        store_vec<float, 4>(a.da + th * a.d + 4 * lane, x);
+      }
+    }
+  for (int m = quads / 2; m; m >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, m);
+  if (used && lane == 0) a.ws[slot] = ds;
+}
+
+template <typename T, int VEC, int L>
+__global__ void __launch_bounds__(kRowThreads, 4) prologue_fwd_kernel(PrologueArgs a, Split p) {
+  if ((int)blockIdx.x >= p.norm.blocks) {
+    gates_fwd(a, p.gate, blockIdx.x - p.norm.blocks);
+    return;
+  }
+  constexpr int U = 2;
+  const int lane = threadIdx.x % L;
+  const int slot = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
+  const int hk = slot % a.Hk, share = a.H / a.Hk;
+  // (all lanes of a warp take every turn: the sums shuffle over whole warps)
+  const long long last = slot < p.norm.slots ? a.tokens : 0;
+  const T *qp = static_cast<const T *>(a.q) + hk * a.d + lane * VEC;
+  const T *kp = static_cast<const T *>(a.k) + hk * a.d + lane * VEC;
+  const long long out = (long long)hk * share * a.d + lane * VEC;
+  const long long turns = (a.tokens + U * p.norm.step - 1) / (U * p.norm.step);
+  long long t = slot / a.Hk;
+  for (long long k = 0; k < turns; ++k) {
+    Raw<T, VEC> raw[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long at = t + u * p.norm.step;
+      raw[u][0] = raw[u][1] = Raw<T, VEC>{};
+      if (at < last) {
+        raw[u][0] = load_raw<T, VEC>(qp + at * a.q_stride);
+        raw[u][1] = load_raw<T, VEC>(kp + at * a.k_stride);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u, t += p.norm.step)
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        float x[VEC];
+        unpack<T, VEC>(raw[u][which], x);
+        if (a.norm_qk & (which ? GDR_NORM_K : GDR_NORM_Q)) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) ss += x[e] * x[e];
+          const float r = rsqrtf(lanes_sum<L>(ss) + kNormEps);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) x[e] *= r;
+        }
+        T *to = static_cast<T *>(which ? a.kn : a.qn) + t * a.H * a.d + out;
+        if (t < last)
+          for (int s = 0; s < share; ++s) store_vec<T, VEC>(to + s * a.d, x);
+      }
+  }
+}
+
+template <typename T, int VEC, int L>
+__global__ void __launch_bounds__(kRowThreads, 3) prologue_bwd_kernel(PrologueArgs a, Split p) {
+  if ((int)blockIdx.x >= p.norm.blocks) {
+    gates_bwd(a, p.gate, blockIdx.x - p.norm.blocks);
     return;
   }
   const int lane = threadIdx.x % L;
-  const int share = a.H / a.Hk;
-  const long long groups = a.tokens * a.Hk;
-  const long long step = (long long)p.norm_blocks * (kRowThreads / L);
-  const long long turns = (groups + step - 1) / step;
-  long long f = (long long)blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
-  for (long long k = 0; k < turns; ++k, f += step) {
-    const bool live = f < groups;
-    const long long t = f / a.Hk;
-    const int hk = (int)(f % a.Hk);
+  const int slot = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
+  const int hk = slot % a.Hk, share = a.H / a.Hk;
+  const long long last = slot < p.norm.slots ? a.tokens : 0;
+  const long long in = (long long)hk * a.d + lane * VEC;
+  const long long up = (long long)hk * share * a.d + lane * VEC;
+  const long long turns = (a.tokens + p.norm.step - 1) / p.norm.step;
+  long long t = slot / a.Hk;
+  for (long long k = 0; k < turns; ++k, t += p.norm.step) {
+    float d[2][VEC] = {};
+    Raw<T, VEC> raw[2] = {};
+    if (t < last) {
+      raw[0] = load_raw<T, VEC>(static_cast<const T *>(a.q) + t * a.q_stride + in);
+      raw[1] = load_raw<T, VEC>(static_cast<const T *>(a.k) + t * a.k_stride + in);
+#pragma unroll 2
+      for (int s = 0; s < share; ++s) {
+        const long long at = (t * a.H + s) * a.d + up;
+        float u[2][VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          load_vec<float, 4>(a.dqn + at + e, &u[0][e]);
+          load_vec<float, 4>(a.dkn + at + e, &u[1][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          d[0][e] += u[0][e];
+          d[1][e] += u[1][e];
+        }
+      }
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const float *up = (which ? a.dkn : a.dqn) + (t * a.H + hk * share) * a.d + lane * VEC;
-      float d[VEC] = {};
-      if (live)
-        for (int s = 0; s < share; ++s) {
-          float u[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; e += 4) load_vec<float, 4>(up + s * a.d + e, u + e);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) d[e] += u[e];
-        }
       if (a.norm_qk & (which ? GDR_NORM_K : GDR_NORM_Q)) {
-        const T *in = static_cast<const T *>(which ? a.k : a.q) +
-                      t * (which ? a.k_stride : a.q_stride) + hk * a.d + lane * VEC;
-        float x[VEC] = {}, ss = 0.f, dot = 0.f;
-        if (live) load_vec<T, VEC>(in, x);
+        float x[VEC], ss = 0.f, dot = 0.f;
+        unpack<T, VEC>(raw[which], x);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           ss += x[e] * x[e];
-          dot += x[e] * d[e];
+          dot += x[e] * d[which][e];
         }
         const float r = rsqrtf(lanes_sum<L>(ss) + kNormEps);
         dot = lanes_sum<L>(dot) * r;  // q^ . G
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) d[e] = r * (d[e] - x[e] * r * dot);
+        for (int e = 0; e < VEC; ++e) d[which][e] = r * (d[which][e] - x[e] * r * dot);
       }
-      T *out = static_cast<T *>(which ? a.dk : a.dq) + f * a.d + lane * VEC;
-      if (live) store_vec<T, VEC>(out, d);
+      if (t < last)
+        store_vec<T, VEC>(static_cast<T *>(which ? a.dk : a.dq) + t * a.Hk * a.d + in, d[which]);
     }
   }
 }
@@ -192,16 +202,15 @@ __global__ void __launch_bounds__(1024) prologue_sum_kernel(const float *part, i
 
 template <bool BWD, typename T, int VEC, int L>
 cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
-  Split p = make_split(a.tokens, a.H, a.d, a.per_channel);
-  p.norm_blocks = blocks_for(a.tokens * a.Hk, kRowThreads / L);
-  const int blocks = p.norm_blocks + p.gate_blocks;
+  const Split p = make_split(a, L);
+  const int blocks = p.norm.blocks + p.gate.blocks;
   if constexpr (!BWD) {
     prologue_fwd_kernel<T, VEC, L><<<blocks, kRowThreads, 0, stream>>>(a, p);
   } else {
     prologue_bwd_kernel<T, VEC, L><<<blocks, kRowThreads, 0, stream>>>(a, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    prologue_sum_kernel<<<(a.H + 31) / 32, 1024, 0, stream>>>(a.ws, (int)p.step, a.H,
+    prologue_sum_kernel<<<(a.H + 31) / 32, 1024, 0, stream>>>(a.ws, (int)p.gate.step, a.H,
                                                              a.dgate_scale);
   }
   return cudaGetLastError();
@@ -220,7 +229,13 @@ cudaError_t launch_d(const PrologueArgs &a, cudaStream_t stream) {
 }  // namespace
 
 size_t prologue_bwd_ws_bytes(long long tokens, int H, int dk, int per_channel) {
-  return (size_t)make_split(tokens, H, dk, per_channel).slots * sizeof(float);
+  PrologueArgs a{};
+  a.tokens = tokens;
+  a.Hk = 1;
+  a.H = H;
+  a.d = dk;
+  a.per_channel = per_channel;
+  return (size_t)make_split(a, 1).gate.slots * sizeof(float);
 }
 
 cudaError_t launch_prologue_fwd(const PrologueArgs &a, cudaStream_t stream) {

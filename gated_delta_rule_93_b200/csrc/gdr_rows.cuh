@@ -6,45 +6,76 @@
 
 namespace gdr {
 
-// The largest grid of the row-wise kernels: 2 blocks of 8 warps for each of the 148 SMs.
-constexpr int kRowBlocks = 2 * 148;
+constexpr int kSMs = 148;
 constexpr int kRowThreads = 256;
 
-// VEC consecutive elements of type T as floats, in one access.
+// Rows of G groups (heads) each, spread over `slots` slots of lanes; a slot
+// keeps its group for all its rows, which are `step` apart.
+struct RowPlan {
+  int blocks, slots;
+  long long step;  // rows between a slot's groups
+};
+
+inline RowPlan row_plan(long long rows, int G, int per_block, int max_blocks) {
+  const long long want = (rows * G + per_block - 1) / per_block;
+  const long long least = ((long long)G + per_block - 1) / per_block;  // every group once
+  long long blocks = want < max_blocks ? want : max_blocks;
+  if (blocks < least) blocks = least;
+  if (blocks < 1) blocks = 1;
+  RowPlan p;
+  p.blocks = (int)blocks;
+  p.step = blocks * per_block / G;
+  p.slots = (int)(p.step * G);
+  return p;
+}
+
+// VEC consecutive elements of type T: one access of `Raw`, unpacked to floats
+// where they are used (a row waits in half the registers as bf16).
 template <int BYTES>
 struct Bits;
 template <> struct Bits<2> { using T = unsigned short; };
 template <> struct Bits<4> { using T = unsigned int; };
 template <> struct Bits<8> { using T = uint2; };
 template <> struct Bits<16> { using T = uint4; };
+template <typename T, int VEC>
+using Raw = typename Bits<sizeof(T) * VEC>::T;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float &d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
 
+// A load of data that is read once (it need not stay in L1).
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float *x) {
-  using B = typename Bits<sizeof(T) * VEC>::T;
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
+  return __ldcs(reinterpret_cast<const Raw<T, VEC> *>(p));
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Raw<T, VEC> &raw, float *x) {
   union {
-    B b;
+    Raw<T, VEC> b;
     T t[VEC];
   } u;
-  u.b = *reinterpret_cast<const B *>(p);
+  u.b = raw;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) x[e] = to_f(u.t[e]);
 }
 
 template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T *p, float *x) {
+  unpack<T, VEC>(load_raw<T, VEC>(p), x);
+}
+
+template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *x) {
-  using B = typename Bits<sizeof(T) * VEC>::T;
   union {
-    B b;
+    Raw<T, VEC> b;
     T t[VEC];
   } u;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) from_f(u.t[e], x[e]);
-  *reinterpret_cast<B *>(p) = u.b;
+  *reinterpret_cast<Raw<T, VEC> *>(p) = u.b;
 }
 
 // The sum over the L lanes (a power of two) that share a row, in all of them.
@@ -56,6 +87,11 @@ __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// The same from the fast exponential and reciprocal: relative error below (4 + |x|) 2^-23,
+// a few instructions instead of about thirty.
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  return __fdividef(1.f, 1.f + __expf(-x));
+}
 // log(1 + e^x), with no branch that overflows.
 __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
