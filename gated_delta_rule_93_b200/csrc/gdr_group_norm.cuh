@@ -4,8 +4,8 @@
 // A group (one head of one token) is a few hundred bytes, so L lanes of a
 // warp hold it in registers: every input is read once, every sum over the
 // group is a few shuffles, every output is written once.  Both directions are
-// bound by HBM as long as enough bytes are in flight: U rows of a lane are
-// requested before the first of them is used.
+// bound by HBM as long as enough bytes are in flight: a lane's next U rows are
+// requested before it works on the U it has.
 //
 // A lane keeps the same group index for all its rows (the number of groups
 // in flight is a multiple of G), so its weights are loaded once.
@@ -19,16 +19,15 @@ inline bool multiple_of(const void *p, size_t bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
-// Elements per access: 16 bytes where every row and group starts on 16; for
-// bf16 also pairs; else single elements.
+// Elements per access: 16 bytes where every row and group starts on 16, for
+// bf16 also 8 bytes; else single elements.
 inline int norm_vector(const GroupNormArgs &a) {
   const int size = a.bf16 ? 2 : 4;
-  for (int vec : {16 / size, 2}) {
-    if (vec == 2 && !a.bf16) break;
-    const size_t bytes = (size_t)vec * size, wide = bytes < 8 ? 8 : 16;  // wide: of fp32 outputs
+  for (int vec : {16 / size, 4}) {
+    const size_t bytes = (size_t)vec * size;
     if (a.D % vec == 0 && a.x_stride % vec == 0 && (!a.z || a.z_stride % vec == 0) &&
         multiple_of(a.x, bytes) && multiple_of(a.z, bytes) && multiple_of(a.dy, bytes) &&
-        multiple_of(a.y, bytes) && multiple_of(a.dz, bytes) && multiple_of(a.dx, wide))
+        multiple_of(a.y, bytes) && multiple_of(a.dz, bytes) && multiple_of(a.dx, 16))
       return vec;
   }
   return 1;
@@ -50,10 +49,8 @@ cudaError_t norm_layout_vec(int D, F f) {
   if constexpr (VEC <= 4) {
     if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
   }
-  if constexpr (VEC <= 2) {
-    if (n <= 512) return f.template operator()<T, VEC, 32, 16>();
-  }
   if constexpr (VEC == 1) {
+    if (n <= 512) return f.template operator()<T, VEC, 32, 16>();
     if (n <= 1024) return f.template operator()<T, VEC, 32, 32>();
   }
   return cudaErrorInvalidValue;
@@ -65,7 +62,7 @@ cudaError_t norm_layout(const GroupNormArgs &a, F f) {
   if (!a.bf16)
     return vec == 4 ? norm_layout_vec<float, 4>(a.D, f) : norm_layout_vec<float, 1>(a.D, f);
   if (vec == 8) return norm_layout_vec<__nv_bfloat16, 8>(a.D, f);
-  return vec == 2 ? norm_layout_vec<__nv_bfloat16, 2>(a.D, f)
+  return vec == 4 ? norm_layout_vec<__nv_bfloat16, 4>(a.D, f)
                   : norm_layout_vec<__nv_bfloat16, 1>(a.D, f);
 }
 

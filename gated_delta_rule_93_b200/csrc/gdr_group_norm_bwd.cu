@@ -3,16 +3,16 @@
 //   dx = rstd (h - [center] mean(h) - n mean(h n)),  dw = sum dl n,  db = sum dl
 //
 // The statistics are computed again from x, which is read anyway.  The weight
-// gradients add up in registers over a lane's rows; then each block (weights
-// shared by the groups) or each row slot (weights per channel) writes one
-// partial row, and a second launch adds the partial rows in a fixed order.
+// gradients add up in registers over a lane's rows, then over the block (with weights per channel
+// a block's slots share a group), and a second launch adds the blocks' partial rows in a fixed
+// order; where one block has all rows of its channels, it writes the gradients itself.
 #include "gdr_group_norm.cuh"
 
 namespace gdr {
 namespace {
 
-// Rows in flight and blocks on an SM for E elements a lane.
-constexpr int rows_ahead(int E) { return E <= 8 ? 2 : 1; }
+// Rows requested at a time (16 bytes of a tensor a lane), and blocks on an SM, for E elements a lane.
+constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
 constexpr int blocks_per_sm(int E) { return E <= 8 ? 2 : 1; }
 
 // Value and slope of the activation.
@@ -22,7 +22,7 @@ __device__ __forceinline__ void act_both(int act, float u, float &f, float &df) 
     df = 1.f;
     return;
   }
-  const float s = fast_sigmoid(u);
+  const float s = sigmoid(u);
   if (act == GDR_ACT_SILU) {
     f = u * s;
     df = s + f * (1.f - s);
@@ -35,11 +35,11 @@ __device__ __forceinline__ void act_both(int act, float u, float &f, float &df) 
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_bwd_kernel(GroupNormArgs a, RowPlan p) {
-  constexpr int E = VEC * NV, U = rows_ahead(E);
+  constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
+  constexpr bool kAhead = E <= 16;  // (wider rows have no registers for a second one)
   constexpr int kPerBlock = kRowThreads / L;
   const int lane = threadIdx.x % L;
-  const int slot = blockIdx.x * kPerBlock + threadIdx.x / L;
-  const int g = slot % a.G;
+  const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
   const float inv_d = 1.f / (float)a.D;
   float w[E], b[E], dw[E], db[E];
   bool in[NV];
@@ -55,26 +55,40 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
       dw[i * VEC + e] = db[i * VEC + e] = 0.f;
     }
   }
-  const long long last = slot < p.slots ? a.rows : 0;  // rows of this slot end here
+  const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
   const long long off = (long long)g * a.D + lane * VEC, dense = (long long)a.G * a.D;
   const T *xp = static_cast<const T *>(a.x) + off, *zp = static_cast<const T *>(a.z) + off;
   const T *dyp = static_cast<const T *>(a.dy) + off;
   const long long turns = (a.rows + U * p.step - 1) / (U * p.step);
-  long long row = slot / a.G;
+  long long row = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
+  Raw<T, VEC> xn[U][NV], zn[U][NV], dyn[U][NV];  // the next turn's rows
+  const auto request = [&](long long from) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const long long at = from + u * p.step;
+        xn[u][i] = zn[u][i] = dyn[u][i] = Raw<T, VEC>{};
+        if (at < last && in[i]) {
+          xn[u][i] = load_raw<T, VEC>(xp + at * a.x_stride + i * L * VEC);
+          dyn[u][i] = load_raw<T, VEC>(dyp + at * dense + i * L * VEC);
+          if (a.z) zn[u][i] = load_raw<T, VEC>(zp + at * a.z_stride + i * L * VEC);
+        }
+      }
+  };
+  if constexpr (kAhead) request(row);
   for (long long k = 0; k < turns; ++k) {
+    if constexpr (!kAhead) request(row);
     Raw<T, VEC> xr[U][NV], zr[U][NV], dyr[U][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const long long at = row + u * p.step;
-        xr[u][i] = zr[u][i] = dyr[u][i] = Raw<T, VEC>{};
-        if (at < last && in[i]) {
-          xr[u][i] = load_raw<T, VEC>(xp + at * a.x_stride + i * L * VEC);
-          dyr[u][i] = load_raw<T, VEC>(dyp + at * dense + i * L * VEC);
-          if (a.z) zr[u][i] = load_raw<T, VEC>(zp + at * a.z_stride + i * L * VEC);
-        }
+        xr[u][i] = xn[u][i];
+        zr[u][i] = zn[u][i];
+        dyr[u][i] = dyn[u][i];
       }
+    if constexpr (kAhead) request(row + U * p.step);
 #pragma unroll
     for (int u = 0; u < U; ++u, row += p.step) {
       float x[E], m = 0.f, ss = 0.f;
@@ -137,40 +151,33 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     }
   }
 
-  // Partial rows of the weight gradients, db behind dw.
+  // Partial rows of the weight gradients, a block's D values each, db behind dw:
+  // over the slots of a warp, then over the warps.
   if (!a.dweight && !a.dbias) return;
-  if (a.per_channel) {  // [step][G D]
-    if (slot < p.slots) {
-      float *pw = a.ws + (long long)slot * a.D;
-      float *pb = pw + p.step * a.G * a.D;
+  __shared__ float s[kRowThreads / 32][L * E];
+  const int warp = threadIdx.x / 32, at = threadIdx.x % 32;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+  for (int which = 0; which < 2; ++which) {
+    float *out = which ? a.dbias : a.dweight;
+    if (!out) continue;
+    if (p.sum) out = a.ws + ((which ? (long long)p.blocks : 0) + blockIdx.x) * a.D;
+    else if (p.by_block) out += (long long)g * a.D;
+    __syncthreads();
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (in[i]) {
-            pw[(i * L + lane) * VEC + e] = dw[i * VEC + e];
-            pb[(i * L + lane) * VEC + e] = db[i * VEC + e];
-          }
+    for (int e = 0; e < E; ++e) {
+      float v = which ? db[e] : dw[e];
+#pragma unroll
+      for (int m = L; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+      // (element e of a lane is channel ((e / VEC) L + lane) VEC + e % VEC)
+      if (at < L) s[warp][((e / VEC) * L + lane) * VEC + e % VEC] = v;
     }
-  } else {  // [blocks][D]
-    __shared__ float s[kRowThreads];
-    float *pw = a.ws + (long long)blockIdx.x * a.D;
-    float *pb = pw + (long long)p.blocks * a.D;
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.D; c += kRowThreads) {
+      float v = 0.f;
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        __syncthreads();
-        s[threadIdx.x] = which ? db[e] : dw[e];
-        __syncthreads();
-        if (threadIdx.x < L) {
-          float v = 0.f;
-#pragma unroll
-          for (int i = 0; i < kPerBlock; ++i) v += s[i * L + lane];
-          const int c = ((e / VEC) * L + lane) * VEC + e % VEC;
-          if (c < a.D) (which ? pb : pw)[c] = v;
-        }
-      }
+      for (int i = 0; i < kRowThreads / 32; ++i) v += s[i][c];
+      out[c] = v;
+    }
   }
 }
 
@@ -182,21 +189,32 @@ __global__ void __launch_bounds__(1024) group_norm_sum_kernel(const float *part,
     sum_columns(part + (blockIdx.y ? (size_t)rows * cols : 0), rows, cols, out, blockIdx.x);
 }
 
+constexpr int kFewTurns = 4;  // rows a slot takes rather than have a second launch
+
+RowPlan bwd_plan(long long rows, int G, int lanes, int per_sm, int per_channel) {
+  const int per_block = kRowThreads / lanes;
+  RowPlan p = row_plan(rows, G, per_block, kSMs * per_sm, per_channel);
+  // few rows: as few blocks as have every channel once
+  if (per_channel ? rows <= kFewTurns * per_block : rows * G <= kFewTurns * per_block)
+    p = row_plan(rows, G, per_block, per_channel ? G : 1, per_channel);
+  p.sum = p.blocks > (per_channel ? G : 1);
+  return p;
+}
+
 struct Launch {
   const GroupNormArgs &a;
   cudaStream_t stream;
   template <typename T, int VEC, int L, int NV>
   cudaError_t operator()() const {
-    const RowPlan p =
-        row_plan(a.rows, a.G, kRowThreads / L, kSMs * blocks_per_sm(VEC * NV));
+    const RowPlan p = bwd_plan(a.rows, a.G, L, blocks_per_sm(VEC * NV), a.per_channel);
     group_norm_bwd_kernel<T, VEC, L, NV><<<p.blocks, kRowThreads, 0, stream>>>(a, p);
-    if (a.dweight || a.dbias) {
+    if (p.sum && (a.dweight || a.dbias)) {
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      const int rows = a.per_channel ? (int)p.step : p.blocks;
+      const int rows = a.per_channel ? p.blocks / a.G : p.blocks;
       const int cols = a.per_channel ? a.G * a.D : a.D;
-      group_norm_sum_kernel<<<dim3((cols + 31) / 32, 2), 1024, 0, stream>>>(a.ws, rows, cols,
-                                                                           a.dweight, a.dbias);
+      const dim3 grid((cols + sum_width(cols) - 1) / sum_width(cols), a.dbias ? 2 : 1);
+      group_norm_sum_kernel<<<grid, 1024, 0, stream>>>(a.ws, rows, cols, a.dweight, a.dbias);
     }
     return cudaGetLastError();
   }
@@ -206,14 +224,13 @@ struct Launch {
 
 size_t group_norm_bwd_ws_bytes(long long rows, int G, int D, int, int per_channel) {
   // the widest grid that any layout of these sizes takes (4 to 32 lanes a group)
-  size_t most = 0;
+  int most = 0;
   for (int lanes = 4; lanes <= 32; lanes *= 2)
     for (int per_sm = 1; per_sm <= blocks_per_sm(1); ++per_sm) {
-      const RowPlan p = row_plan(rows, G, kRowThreads / lanes, kSMs * per_sm);
-      const size_t part = per_channel ? (size_t)p.step * G * D : (size_t)p.blocks * D;
-      if (part > most) most = part;
+      const RowPlan p = bwd_plan(rows, G, lanes, per_sm, per_channel);
+      if (p.blocks > most) most = p.blocks;
     }
-  return 2 * most * sizeof(float);
+  return 2 * (size_t)most * D * sizeof(float);
 }
 
 cudaError_t launch_group_norm_bwd(const GroupNormArgs &a, cudaStream_t stream) {

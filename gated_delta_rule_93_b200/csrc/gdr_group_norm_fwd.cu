@@ -5,23 +5,24 @@
 namespace gdr {
 namespace {
 
-// Rows in flight and blocks on an SM for E elements a lane.
-constexpr int rows_ahead(int E) { return E <= 8 ? 2 : 1; }
+// Rows requested at a time (16 bytes of a tensor a lane), and blocks on an SM, for E elements a lane.
+constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
 constexpr int blocks_per_sm(int E) { return E <= 8 ? 4 : E <= 16 ? 2 : 1; }
 
 __device__ __forceinline__ float act_of(int act, float u) {
   if (act == GDR_ACT_NONE) return u;
-  const float s = fast_sigmoid(u);
+  const float s = sigmoid(u);
   return act == GDR_ACT_SILU ? u * s : s;
 }
 
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_fwd_kernel(GroupNormArgs a, RowPlan p) {
-  constexpr int E = VEC * NV, U = rows_ahead(E);
+  constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
+  constexpr bool kAhead = E <= 16;  // (wider rows have no registers for a second one)
   const int lane = threadIdx.x % L;
-  const int slot = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
-  const int g = slot % a.G;
+  constexpr int kPerBlock = kRowThreads / L;
+  const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
   const float inv_d = 1.f / (float)a.D;
   float w[E], b[E];
   bool in[NV];
@@ -37,25 +38,38 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     }
   }
   // (all lanes of a warp take every turn: the sums shuffle over whole warps)
-  const long long last = slot < p.slots ? a.rows : 0;  // rows of this slot end here
+  const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
   const T *xp = static_cast<const T *>(a.x) + (long long)g * a.D + lane * VEC;
   const T *zp = static_cast<const T *>(a.z) + (long long)g * a.D + lane * VEC;
   T *yp = static_cast<T *>(a.y) + (long long)g * a.D + lane * VEC;
   const long long turns = (a.rows + U * p.step - 1) / (U * p.step);
-  long long row = slot / a.G;
+  long long row = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
+  Raw<T, VEC> xn[U][NV], zn[U][NV];  // the next turn's rows
+  const auto request = [&](long long from) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const long long at = from + u * p.step;
+        xn[u][i] = zn[u][i] = Raw<T, VEC>{};
+        if (at < last && in[i]) {
+          xn[u][i] = load_raw<T, VEC>(xp + at * a.x_stride + i * L * VEC);
+          if (a.z) zn[u][i] = load_raw<T, VEC>(zp + at * a.z_stride + i * L * VEC);
+        }
+      }
+  };
+  if constexpr (kAhead) request(row);
   for (long long k = 0; k < turns; ++k) {
+    if constexpr (!kAhead) request(row);
     Raw<T, VEC> xr[U][NV], zr[U][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const long long at = row + u * p.step;
-        xr[u][i] = zr[u][i] = Raw<T, VEC>{};
-        if (at < last && in[i]) {
-          xr[u][i] = load_raw<T, VEC>(xp + at * a.x_stride + i * L * VEC);
-          if (a.z) zr[u][i] = load_raw<T, VEC>(zp + at * a.z_stride + i * L * VEC);
-        }
+        xr[u][i] = xn[u][i];
+        zr[u][i] = zn[u][i];
       }
+    if constexpr (kAhead) request(row + U * p.step);
 #pragma unroll
     for (int u = 0; u < U; ++u, row += p.step) {
       float x[E], m = 0.f, ss = 0.f;
@@ -97,7 +111,7 @@ struct Launch {
   template <typename T, int VEC, int L, int NV>
   cudaError_t operator()() const {
     const RowPlan p =
-        row_plan(a.rows, a.G, kRowThreads / L, kSMs * blocks_per_sm(VEC * NV));
+        row_plan(a.rows, a.G, kRowThreads / L, kSMs * blocks_per_sm(VEC * NV), false);
     group_norm_fwd_kernel<T, VEC, L, NV><<<p.blocks, kRowThreads, 0, stream>>>(a, p);
     return cudaGetLastError();
   }

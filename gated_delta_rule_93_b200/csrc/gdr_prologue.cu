@@ -12,100 +12,163 @@
 // U tokens of q and k requested before the first is used.  The gates are the work
 // of other blocks of the same launch: a thread for a (token, head) with a
 // scalar gate, dk / 4 lanes with a per-channel one.  Every slot keeps its head
-// for all its tokens (no division in the loops), so ds adds up in registers;
-// a second launch adds the slots' sums in a fixed order.
+// for all its tokens (no division in the loops), so ds adds up in registers
+// and then over the block; a second launch adds the blocks' sums in a fixed
+// order, unless one block had all tokens.
 #include "gdr_rows.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr float kNormEps = 1e-6f;
-constexpr int kMaxBlocks = 4 * kSMs;  // of each kind of work
+constexpr int kNormBlocks = 4 * kSMs, kGateBlocks = 8 * kSMs;  // at most
 
-struct Split {
-  RowPlan norm, gate;
+// The gates' blocks: `heads` heads of `tokens` tokens at a time; blocks that
+// share a tile of heads are `step` tokens apart.
+struct GatePlan {
+  int blocks, heads, tiles, tokens;
+  long long step;
 };
 
-Split make_split(const PrologueArgs &a, int L) {
-  const int lanes = a.per_channel ? a.d / 4 : 1;
-  return {row_plan(a.tokens, a.Hk, kRowThreads / L, kMaxBlocks),
-          row_plan(a.tokens, a.H, kRowThreads / lanes, kMaxBlocks)};
+struct Split {
+  RowPlan norm;
+  GatePlan gate;
+};
+
+// A thread for a (token, head) with a scalar gate, dk / 4 lanes with a
+// per-channel one (a block then has one head).
+GatePlan gate_plan(long long tokens, int H, int dk, int per_channel) {
+  GatePlan p;
+  const int slots = kRowThreads / (per_channel ? dk / 4 : 1);
+  p.heads = per_channel ? 1 : H < slots ? H : slots;
+  p.tiles = (H + p.heads - 1) / p.heads;
+  p.tokens = slots / p.heads;
+  long long rows = (tokens + p.tokens - 1) / p.tokens;
+  if (rows > kGateBlocks / p.tiles) rows = kGateBlocks / p.tiles;
+  if (rows < 1) rows = 1;
+  p.blocks = (int)(rows * p.tiles);
+  p.step = rows * p.tokens;
+  return p;
 }
 
-// g and beta of one block's gate slots.
-__device__ __forceinline__ void gates_fwd(const PrologueArgs &a, const RowPlan &p, int block) {
-  const int thread = block * kRowThreads + threadIdx.x;
-  const int quads = a.per_channel ? a.d / 4 : 1, slot = thread / quads, lane = thread % quads;
-  if (slot >= p.slots) return;
-  const int h = slot % a.H;
-  const float s = -a.gate_scale[h];
-  for (long long t = slot / a.H; t < a.tokens; t += p.step) {
-    const long long th = t * a.H + h;
-    if (lane == 0) a.beta[th] = sigmoid(a.b[th]);
+// The place of a thread among its block's gates.
+struct GatePlace {
+  int h, lane;
+  long long token;
+  bool used;
+};
+__device__ __forceinline__ GatePlace gate_place(const PrologueArgs &a, const GatePlan &p, int block) {
+  const int quads = a.per_channel ? a.d / 4 : 1, slot = threadIdx.x / quads;
+  GatePlace g;
+  g.lane = threadIdx.x % quads;
+  g.h = block % p.tiles * p.heads + slot % p.heads;
+  g.token = (long long)(block / p.tiles) * p.tokens + slot / p.heads;
+  g.used = g.h < a.H && slot < p.tokens * p.heads;
+  return g;
+}
+
+// g and beta of one block's gates.
+__device__ __forceinline__ void gates_fwd(const PrologueArgs &a, const GatePlan &p, int block) {
+  const GatePlace g = gate_place(a, p, block);
+  if (!g.used) return;
+  const float s = -a.gate_scale[g.h];
+#pragma unroll 2
+  for (long long t = g.token; t < a.tokens; t += p.step) {
+    const long long th = t * a.H + g.h;
+    if (g.lane == 0) a.beta[th] = sigmoid(__ldcs(a.b + th));
     if (!a.per_channel) {
-      a.g[th] = s * softplus(a.a[th]);
+      a.g[th] = s * softplus(__ldcs(a.a + th));
     } else {
       float x[4];
-      load_vec<float, 4>(a.a + th * a.d + 4 * lane, x);
+      load_vec<float, 4>(a.a + th * a.d + 4 * g.lane, x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = s * softplus(x[e]);
-      store_vec<float, 4>(a.g + th * a.d + 4 * lane, x);
+      store_vec<float, 4>(a.g + th * a.d + 4 * g.lane, x);
     }
   }
 }
 
-// da, db and the slot's part of ds.
-__device__ __forceinline__ void gates_bwd(const PrologueArgs &a, const RowPlan &p, int block) {
-  const int thread = block * kRowThreads + threadIdx.x;
-  const int quads = a.per_channel ? a.d / 4 : 1, slot = thread / quads, lane = thread % quads;
-  const bool used = slot < p.slots;
-  const int h = slot % a.H;
-  const float s = a.gate_scale[h];
+// da, db and the block's part of ds: [blocks / tiles][H].
+__device__ __forceinline__ void gates_bwd(const PrologueArgs &a, const GatePlan &p, int block) {
+  constexpr int U = 2;
+  const GatePlace g = gate_place(a, p, block);
   float ds = 0.f;
-  if (used)
-    for (long long t = slot / a.H; t < a.tokens; t += p.step) {
-      const long long th = t * a.H + h;
-      if (lane == 0) {
-        const float beta = sigmoid(a.b[th]);
-        a.db[th] = beta * (1.f - beta) * a.dbeta[th];
+  if (g.used) {
+    const float s = a.gate_scale[g.h];
+    for (long long t = g.token; t < a.tokens; t += U * p.step) {
+      float b[U], dbeta[U], x[U][4], dg[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long at = t + u * p.step, th = at * a.H + g.h;
+        if (at >= a.tokens) continue;
+        if (g.lane == 0) {
+          b[u] = __ldcs(a.b + th);
+          dbeta[u] = __ldcs(a.dbeta + th);
+        }
+        if (!a.per_channel) {
+          x[u][0] = __ldcs(a.a + th);
+          dg[u][0] = __ldcs(a.dg + th);
+        } else {
+          load_vec<float, 4>(a.a + th * a.d + 4 * g.lane, x[u]);
+          load_vec<float, 4>(a.dg + th * a.d + 4 * g.lane, dg[u]);
+        }
       }
-      if (!a.per_channel) {
-        const float x = a.a[th], dg = a.dg[th];
-        a.da[th] = -s * sigmoid(x) * dg;
-        ds -= dg * softplus(x);
-      } else {
-        float x[4], dg[4];
-        load_vec<float, 4>(a.a + th * a.d + 4 * lane, x);
-        load_vec<float, 4>(a.dg + th * a.d + 4 * lane, dg);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long at = t + u * p.step, th = at * a.H + g.h;
+        if (at >= a.tokens) continue;
+        if (g.lane == 0) {
+          const float beta = sigmoid(b[u]);
+          a.db[th] = beta * (1.f - beta) * dbeta[u];
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          ds -= dg[e] * softplus(x[e]);
-          x[e] = -s * sigmoid(x[e]) * dg[e];
+          if (e && !a.per_channel) break;
+          float sig;
+          ds -= dg[u][e] * softplus(x[u][e], &sig);
+          x[u][e] = -s * sig * dg[u][e];
         }
-        store_vec<float, 4>(a.da + th * a.d + 4 * lane, x);
+        if (!a.per_channel)
+          a.da[th] = x[u][0];
+        else
+          store_vec<float, 4>(a.da + th * a.d + 4 * g.lane, x[u]);
       }
     }
+  }
+  // over the lanes of a head (a power of two of them, whole warps or less), then over its slots
+  const int quads = a.per_channel ? a.d / 4 : 1;
   for (int m = quads / 2; m; m >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, m);
-  if (used && lane == 0) a.ws[slot] = ds;
+  __shared__ float part[kRowThreads];
+  if (g.lane == 0) part[threadIdx.x / quads] = ds;
+  __syncthreads();
+  const int mine = threadIdx.x, h = block % p.tiles * p.heads + mine;
+  if (mine < p.heads && h < a.H) {
+    float v = 0.f;
+    for (int i = 0; i < p.tokens; ++i) v += part[i * p.heads + mine];
+    const bool all = p.blocks == p.tiles;  // this block had all tokens
+    (all ? a.dgate_scale : a.ws + (long long)(block / p.tiles) * a.H)[h] = v;
+  }
 }
 
 template <typename T, int VEC, int L>
 __global__ void __launch_bounds__(kRowThreads, 4) prologue_fwd_kernel(PrologueArgs a, Split p) {
-  if ((int)blockIdx.x >= p.norm.blocks) {
-    gates_fwd(a, p.gate, blockIdx.x - p.norm.blocks);
+  const int block = blockIdx.x;
+  if (block >= p.norm.blocks) {
+    gates_fwd(a, p.gate, block - p.norm.blocks);
     return;
   }
   constexpr int U = 2;
   const int lane = threadIdx.x % L;
-  const int slot = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
-  const int hk = slot % a.Hk, share = a.H / a.Hk;
+  constexpr int kPerBlock = kRowThreads / L;
+  const int slot = threadIdx.x / L, hk = p.norm.group(block, slot, kPerBlock, a.Hk);
+  const int share = a.H / a.Hk;
   // (all lanes of a warp take every turn: the sums shuffle over whole warps)
-  const long long last = slot < p.norm.slots ? a.tokens : 0;
+  const long long last = p.norm.used(block, slot, kPerBlock) ? a.tokens : 0;
   const T *qp = static_cast<const T *>(a.q) + hk * a.d + lane * VEC;
   const T *kp = static_cast<const T *>(a.k) + hk * a.d + lane * VEC;
   const long long out = (long long)hk * share * a.d + lane * VEC;
   const long long turns = (a.tokens + U * p.norm.step - 1) / (U * p.norm.step);
-  long long t = slot / a.Hk;
+  long long t = p.norm.first_row(block, slot, kPerBlock, a.Hk);
   for (long long k = 0; k < turns; ++k) {
     Raw<T, VEC> raw[U][2];
 #pragma unroll
@@ -140,18 +203,20 @@ __global__ void __launch_bounds__(kRowThreads, 4) prologue_fwd_kernel(PrologueAr
 
 template <typename T, int VEC, int L>
 __global__ void __launch_bounds__(kRowThreads, 3) prologue_bwd_kernel(PrologueArgs a, Split p) {
-  if ((int)blockIdx.x >= p.norm.blocks) {
-    gates_bwd(a, p.gate, blockIdx.x - p.norm.blocks);
+  if ((int)blockIdx.x < p.gate.blocks) {
+    gates_bwd(a, p.gate, blockIdx.x);
     return;
   }
+  const int block = blockIdx.x - p.gate.blocks;
   const int lane = threadIdx.x % L;
-  const int slot = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;
-  const int hk = slot % a.Hk, share = a.H / a.Hk;
-  const long long last = slot < p.norm.slots ? a.tokens : 0;
+  constexpr int kPerBlock = kRowThreads / L;
+  const int slot = threadIdx.x / L, hk = p.norm.group(block, slot, kPerBlock, a.Hk);
+  const int share = a.H / a.Hk;
+  const long long last = p.norm.used(block, slot, kPerBlock) ? a.tokens : 0;
   const long long in = (long long)hk * a.d + lane * VEC;
   const long long up = (long long)hk * share * a.d + lane * VEC;
   const long long turns = (a.tokens + p.norm.step - 1) / p.norm.step;
-  long long t = slot / a.Hk;
+  long long t = p.norm.first_row(block, slot, kPerBlock, a.Hk);
   for (long long k = 0; k < turns; ++k, t += p.norm.step) {
     float d[2][VEC] = {};
     Raw<T, VEC> raw[2] = {};
@@ -202,16 +267,19 @@ __global__ void __launch_bounds__(1024) prologue_sum_kernel(const float *part, i
 
 template <bool BWD, typename T, int VEC, int L>
 cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
-  const Split p = make_split(a, L);
+  const Split p = {row_plan(a.tokens, a.Hk, kRowThreads / L, kNormBlocks, false),
+                   gate_plan(a.tokens, a.H, a.d, a.per_channel)};
   const int blocks = p.norm.blocks + p.gate.blocks;
   if constexpr (!BWD) {
     prologue_fwd_kernel<T, VEC, L><<<blocks, kRowThreads, 0, stream>>>(a, p);
   } else {
     prologue_bwd_kernel<T, VEC, L><<<blocks, kRowThreads, 0, stream>>>(a, p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    prologue_sum_kernel<<<(a.H + 31) / 32, 1024, 0, stream>>>(a.ws, (int)p.gate.step, a.H,
-                                                             a.dgate_scale);
+    if (p.gate.blocks > p.gate.tiles) {
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      prologue_sum_kernel<<<(a.H + sum_width(a.H) - 1) / sum_width(a.H), 1024, 0, stream>>>(
+          a.ws, p.gate.blocks / p.gate.tiles, a.H, a.dgate_scale);
+    }
   }
   return cudaGetLastError();
 }
@@ -229,13 +297,8 @@ cudaError_t launch_d(const PrologueArgs &a, cudaStream_t stream) {
 }  // namespace
 
 size_t prologue_bwd_ws_bytes(long long tokens, int H, int dk, int per_channel) {
-  PrologueArgs a{};
-  a.tokens = tokens;
-  a.Hk = 1;
-  a.H = H;
-  a.d = dk;
-  a.per_channel = per_channel;
-  return (size_t)make_split(a, 1).gate.slots * sizeof(float);
+  const GatePlan p = gate_plan(tokens, H, dk, per_channel);
+  return (size_t)(p.blocks / p.tiles) * H * sizeof(float);
 }
 
 cudaError_t launch_prologue_fwd(const PrologueArgs &a, cudaStream_t stream) {

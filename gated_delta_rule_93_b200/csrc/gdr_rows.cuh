@@ -9,23 +9,43 @@ namespace gdr {
 constexpr int kSMs = 148;
 constexpr int kRowThreads = 256;
 
-// Rows of G groups (heads) each, spread over `slots` slots of lanes; a slot
-// keeps its group for all its rows, which are `step` apart.
+// How the rows of G groups (heads) each are spread over a grid: slots of
+// lanes take a group each and keep it for all their rows, `step` apart.
+//   by slot:  consecutive slots take consecutive groups;
+//   by block: the slots of a block share a group (sums over rows then end in
+//             one value a block and channel).
 struct RowPlan {
-  int blocks, slots;
-  long long step;  // rows between a slot's groups
+  int blocks;
+  int slots;  // in use (by slot: a multiple of G)
+  int by_block;
+  int sum;  // whether partial rows are left for a second launch
+  long long step;
+
+  __device__ __forceinline__ int group(int block, int slot_in_block, int per_block, int G) const {
+    return by_block ? block % G : (block * per_block + slot_in_block) % G;
+  }
+  __device__ __forceinline__ long long first_row(int block, int slot_in_block, int per_block,
+                                                 int G) const {
+    return by_block ? (long long)(block / G) * per_block + slot_in_block
+                    : (block * per_block + slot_in_block) / G;
+  }
+  __device__ __forceinline__ bool used(int block, int slot_in_block, int per_block) const {
+    return by_block || block * per_block + slot_in_block < slots;
+  }
 };
 
-inline RowPlan row_plan(long long rows, int G, int per_block, int max_blocks) {
-  const long long want = (rows * G + per_block - 1) / per_block;
-  const long long least = ((long long)G + per_block - 1) / per_block;  // every group once
-  long long blocks = want < max_blocks ? want : max_blocks;
-  if (blocks < least) blocks = least;
-  if (blocks < 1) blocks = 1;
+inline RowPlan row_plan(long long rows, int G, int per_block, int max_blocks, bool by_block) {
+  const long long least = by_block ? G : ((long long)G + per_block - 1) / per_block;
+  long long blocks = by_block ? (rows + per_block - 1) / per_block * G
+                              : (rows * G + per_block - 1) / per_block;
+  if (blocks > max_blocks) blocks = by_block ? max_blocks / G * G : max_blocks;
+  if (blocks < least) blocks = least;  // every group once
   RowPlan p;
   p.blocks = (int)blocks;
-  p.step = blocks * per_block / G;
-  p.slots = (int)(p.step * G);
+  p.by_block = by_block;
+  p.sum = 0;
+  p.step = by_block ? blocks / G * per_block : blocks * per_block / G;
+  p.slots = (int)(by_block ? blocks * per_block : p.step * G);
   return p;
 }
 
@@ -86,35 +106,44 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
-// The same from the fast exponential and reciprocal: relative error below (4 + |x|) 2^-23,
-// a few instructions instead of about thirty.
-__device__ __forceinline__ float fast_sigmoid(float x) {
-  return __fdividef(1.f, 1.f + __expf(-x));
-}
-// log(1 + e^x), with no branch that overflows.
-__device__ __forceinline__ float softplus(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+// Fast exponential and reciprocal: relative error below (4 + |x|) 2^-23, a few
+// instructions instead of about thirty.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// log(1 + e^x), with no branch that overflows, and 1 / (1 + e^-x) from the same exponential.
+__device__ __forceinline__ float softplus(float x, float *sig = nullptr) {
+  const float e = __expf(-fabsf(x));
+  if (sig) *sig = __fdividef(x >= 0.f ? 1.f : e, 1.f + e);
+  return fmaxf(x, 0.f) + log1pf(e);
 }
 
-// out[c] = sum over k of part[k * cols + c], in a fixed order: a block takes
-// 32 columns, its 32 row threads every 32nd row each, then one thread a column.
+// out[c] = sum over k of part[k * cols + c], in a fixed order.  A block of 1024
+// threads takes W columns (a power of two up to 32, fewer where there are
+// few columns, so that more threads share one) and adds up in a tree.
+__host__ __device__ __forceinline__ int sum_width(int cols) {
+  return cols <= 4 ? 4 : cols <= 8 ? 8 : cols <= 16 ? 16 : 32;
+}
 __device__ __forceinline__ void sum_columns(const float *part, int rows, int cols, float *out,
                                             int block) {
-  __shared__ float s[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int c = block * 32 + x;
-  float v = 0.f;
-  if (c < cols)
-    for (int k = y; k < rows; k += 32) v += part[(size_t)k * cols + c];
-  s[y][x] = v;
-  __syncthreads();
-  if (y == 0) {
-    v = 0.f;
+  __shared__ float s[1024];
+  const int W = sum_width(cols), Y = 1024 / W;
+  const int x = threadIdx.x % W, y = threadIdx.x / W;
+  const int c = block * W + x;
+  float v[4] = {};
+  if (c < cols) {
+    int k = y;
+    for (; k + 3 * Y < rows; k += 4 * Y)
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v += s[k][x];
-    if (c < cols) out[c] = v;
+      for (int i = 0; i < 4; ++i) v[i] += part[(size_t)(k + i * Y) * cols + c];
+    for (; k < rows; k += Y) v[0] += part[(size_t)k * cols + c];
   }
+  s[threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
+  __syncthreads();
+  for (int n = 512; n >= W; n >>= 1) {
+    if ((int)threadIdx.x < n) s[threadIdx.x] += s[threadIdx.x + n];
+    __syncthreads();
+  }
+  if ((int)threadIdx.x < W && c < cols) out[c] = s[threadIdx.x];
 }
 
 }  // namespace gdr

@@ -6,8 +6,8 @@
 // S' = S Diag(alpha):
 //     p_i = S'_i . k,  r_i = S'_i . q,  u_i = beta (v_i - p_i)
 //     S_i <- S'_i + u_i k^T,  o_i = r_i + u_i (k . q)
-// Rows are independent, so a thread block takes 16 RPT rows of one (request,
-// value head), reads them once, runs the request's tokens with the rows in
+// Rows are independent, so a thread block takes 64 rows of one (request,
+// value head; 32 where dv is 32), reads them once, runs the request's tokens with the rows in
 // registers and writes them wherever the request keeps a state.  One token a
 // request moves 2 * 4 * dk * dv bytes per (request, head) for 7 dk dv flops:
 // bound by HBM.
@@ -15,25 +15,64 @@
 // Layout: 8 lanes share a row, lane l of them holding the float4s at columns
 // 32 c + 4 l: a warp's load is four whole 128-byte lines, and a row's two dot
 // products need 3 shuffle steps instead of 5.  What all rows of a head share (k, q
-// with their norms, the gates, k . q) is prepared once per block, a warp per
-// token, in shared memory, while the state's loads are in flight.
+// with their norms, the gates, k . q) is prepared once per block in shared
+// memory, 8 tokens at a time, a warp each: the first 8 while the state's loads are in flight.
 #include "gdr_internal.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTokens = 4;  // tokens prepared at a time, a warp each
+constexpr int kRpt = 2;  // rows per thread, 4 threads apart
+constexpr int rows_of(int warps) { return 4 * kRpt * warps; }  // of a block
+
 constexpr float kNormEps = 1e-6f;
 
-template <int DK, bool PERCH>
-struct __align__(16) Prepared {
-  float k[kTokens][DK];
-  float q[kTokens][DK];
-  float al[kTokens][PERCH ? DK : 4];
-  float beta[kTokens], kq[kTokens];
-  int dst[kTokens];
+template <int DK, int WARPS, bool PERCH>
+struct __align__(16) Prepared {  // a token a warp
+  float k[WARPS][DK];
+  float q[WARPS][DK];
+  float al[WARPS][PERCH ? DK : 4];
+  float v[WARPS][rows_of(WARPS)];
+  float beta[WARPS], kq[WARPS];
+  int dst[WARPS];
 };
+
+// VEC consecutive values of a lane: q, k, v or a gate, and the state's (read once).
+template <int VEC, bool BF16>
+__device__ __forceinline__ void load_lane(const void *p, size_t i, float (&x)[VEC]) {
+  if constexpr (!BF16 && VEC == 4) {
+    const float4 t = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+  } else if constexpr (BF16 && VEC == 4) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+    x[0] = __uint_as_float(t.x << 16); x[1] = __uint_as_float(t.x & 0xffff0000u);
+    x[2] = __uint_as_float(t.y << 16); x[3] = __uint_as_float(t.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = load_in(p, i + e, BF16);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_lane_stream(const float *p, float (&x)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 t = __ldcs(reinterpret_cast<const float4 *>(p));
+    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+  } else if constexpr (VEC == 2) {
+    const float2 t = __ldcs(reinterpret_cast<const float2 *>(p));
+    x[0] = t.x; x[1] = t.y;
+  } else {
+    x[0] = __ldcs(p);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_lane_stream(float *p, const float (&x)[VEC]) {
+  if constexpr (VEC == 4)
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+  else if constexpr (VEC == 2)
+    __stcs(reinterpret_cast<float2 *>(p), make_float2(x[0], x[1]));
+  else
+    __stcs(p, x[0]);
+}
 
 // log(1 + e^x), with no branch that overflows.
 __device__ __forceinline__ float softplus(float x) {
@@ -45,6 +84,25 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
   return x;
 }
+
+// Two fp32 products or multiply-adds in one instruction.
+__device__ __forceinline__ unsigned long long bits(float2 x) {
+  return *reinterpret_cast<unsigned long long *>(&x);
+}
+__device__ __forceinline__ float2 pair(unsigned long long x) {
+  return *reinterpret_cast<float2 *>(&x);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Sum NV per-lane values over groups of 8 lanes, halving the values while the
 // lane masks allow it: afterwards a lane holds the sum of value (lane & 7) >> SH,
@@ -73,19 +131,21 @@ __device__ __forceinline__ float reduce8(float (&x)[NV], int lane) {
   return x[0];
 }
 
-template <int DK, int RPT, bool BF16, bool PERCH>
-__global__ void __launch_bounds__(kWarps * 32) gdr_step_slots_kernel(StepSlotsArgs a) {
-  constexpr int NC = DK / 32;                                 // float4s of a row per lane
-  constexpr int NV = 2 * RPT;                                 // dot products per thread
+template <int DK, int WARPS, bool BF16, bool PERCH>
+__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(StepSlotsArgs a) {
+  constexpr int RPT = kRpt, kRows = rows_of(WARPS);
+  constexpr int NC = DK / 32;  // float4s of a row per lane
+  constexpr int NV = 2 * RPT;  // dot products per thread
   constexpr int SH = NV == 8 ? 0 : NV == 4 ? 1 : 2;
-  __shared__ Prepared<DK, PERCH> sm;
+  __shared__ Prepared<DK, WARPS, PERCH> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int blocks_per_head = a.dv / (kWarps * 4 * RPT);
+  const int blocks_per_head = a.dv / kRows;
   const unsigned rh = blockIdx.x / blocks_per_head;
   const int r = rh / a.H, h = rh % a.H;
   const int hk = h / (a.H / a.Hk);
-  const int row0 = (blockIdx.x % blocks_per_head) * (kWarps * 4 * RPT) + warp * 4 * RPT +
-                   (lane >> 3);  // this thread's rows: row0 + 4 i
+  const int block_row = (blockIdx.x % blocks_per_head) * kRows;
+  const int in_block = warp * 4 * RPT + (lane >> 3);  // this thread's rows: in_block + 4 i
+  const int row0 = block_row + in_block;
   const int col0 = (lane & 7) * 4;
 
   int t0 = r, t1 = r + 1;
@@ -101,66 +161,67 @@ __global__ void __launch_bounds__(kWarps * 32) gdr_step_slots_kernel(StepSlotsAr
   }
   const size_t in_slot = ((size_t)h * a.dv + row0) * DK + col0;
 
-  float s[RPT][NC * 4];
+  float2 s[RPT][2 * NC];
   if (src >= 0) {
     const float *p = a.pool + (size_t)src * a.slot_stride + in_slot;
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        *reinterpret_cast<float4 *>(&s[i][4 * c]) =
-            __ldcs(reinterpret_cast<const float4 *>(p + (size_t)i * 4 * DK + c * 32));
+      for (int c = 0; c < NC; ++c) {
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + i * 4 * DK + c * 32));
+        s[i][2 * c] = make_float2(x.x, x.y);
+        s[i][2 * c + 1] = make_float2(x.z, x.w);
+      }
   } else {
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
 #pragma unroll
-      for (int c = 0; c < NC * 4; ++c) s[i][c] = 0.f;
+      for (int c = 0; c < 2 * NC; ++c) s[i][c] = make_float2(0.f, 0.f);
   }
 
-  for (int tb = t0; tb < t1; tb += kTokens) {
-    const int n = min(kTokens, t1 - tb);
+  for (int tb = t0; tb < t1; tb += WARPS) {
+    const int n = min(WARPS, t1 - tb);
     if (tb != t0) __syncthreads();
-    if (warp < n) {  // warp w prepares token tb + w, DK / 32 channels a lane
-      const size_t t = tb + warp;
-      const size_t th = t * a.H + h;
-      float kv[NC], qv[NC], kk = 0.f, qq = 0.f, kq = 0.f;
+    if (warp < n) {  // warp w prepares token tb + w, DK / 32 channels and some values a lane
+      const size_t t = tb + warp, th = t * a.H + h;
+      float kv[NC], qv[NC], gv[PERCH ? NC : 1];
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
         kv[e] = load_in(a.k, t * a.k_stride + (size_t)hk * DK + lane + 32 * e, BF16);
         qv[e] = load_in(a.q, t * a.q_stride + (size_t)hk * DK + lane + 32 * e, BF16);
+        if constexpr (PERCH) gv[e] = a.g[th * DK + lane + 32 * e];
+      }
+      if constexpr (!PERCH) gv[0] = a.g[th];
+      const float bl = a.beta[th];
+      // where the state goes after this token (-1: nowhere)
+      int d = a.dst ? a.dst[t] : ((int)t == t1 - 1 ? src : -1);
+#pragma unroll
+      for (int e = 0; e < kRows / 32; ++e)
+        sm.v[warp][lane + 32 * e] =
+            load_in(a.v, t * a.v_stride + (size_t)h * a.dv + block_row + lane + 32 * e, BF16);
+      const float scale = a.gate_scale ? a.gate_scale[h] : 0.f;
+      float kk = 0.f, qq = 0.f, kq = 0.f, rk = 1.f, rq = 1.f;
+#pragma unroll
+      for (int e = 0; e < NC; ++e) {
         kk += kv[e] * kv[e];
         qq += qv[e] * qv[e];
         kq += kv[e] * qv[e];
       }
-      float bl = a.beta[th];
-      if (a.gate_scale) bl = 1.f / (1.f + expf(-bl));
-      const float sc = a.gate_scale ? a.gate_scale[h] : 0.f;
-      if constexpr (PERCH) {
-#pragma unroll
-        for (int e = 0; e < NC; ++e) {
-          float g = a.g[th * DK + lane + 32 * e];
-          if (a.gate_scale) g = -sc * softplus(g);
-          sm.al[warp][lane + 32 * e] = expf(g);
-        }
-      } else {
-        float g = a.g[th];
-        if (a.gate_scale) g = -sc * softplus(g);
-        if (lane == 0) sm.al[warp][0] = expf(g);
-      }
       kq = warp_sum(kq);
-      float rk = 1.f, rq = 1.f;
       if (a.norm_qk & GDR_NORM_K) rk = rsqrtf(warp_sum(kk) + kNormEps);
       if (a.norm_qk & GDR_NORM_Q) rq = rsqrtf(warp_sum(qq) + kNormEps);
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
         sm.k[warp][lane + 32 * e] = kv[e] * rk;
         sm.q[warp][lane + 32 * e] = qv[e] * rq;
+        if constexpr (PERCH)
+          sm.al[warp][lane + 32 * e] = expf(a.gate_scale ? -scale * softplus(gv[e]) : gv[e]);
       }
       if (lane == 0) {
-        sm.beta[warp] = bl;
+        if constexpr (!PERCH)
+          sm.al[warp][0] = expf(a.gate_scale ? -scale * softplus(gv[0]) : gv[0]);
+        sm.beta[warp] = a.gate_scale ? 1.f / (1.f + expf(-bl)) : bl;
         sm.kq[warp] = kq * rk * rq;
-        // where the state goes after this token (-1: nowhere)
-        int d = a.dst ? a.dst[t] : (tb + warp == t1 - 1 ? src : -1);
         if (d >= a.slots || d < -1) {
           atomicOr(a.status, kStatusSlot);
           d = -1;
@@ -173,24 +234,35 @@ __global__ void __launch_bounds__(kWarps * 32) gdr_step_slots_kernel(StepSlotsAr
       const size_t to = ((size_t)(tb + j) * a.H + h) * a.dv;
       const int idx = (lane & 7) >> SH;   // the dot product this lane ends up with
       const int mine = idx % RPT;         // its row: p for idx < RPT, r after
-      const float v = load_in(a.v, (size_t)(tb + j) * a.v_stride + (size_t)h * a.dv + row0 + 4 * mine,
-                              BF16);
-      float part[NV] = {};
-      float al0 = 0.f;
-      if constexpr (!PERCH) al0 = sm.al[j][0];
+      const float v = sm.v[j][in_block + 4 * mine];
+      float2 p2[RPT] = {}, r2[RPT] = {};
+      float2 al = both(0.f);
+      if constexpr (!PERCH) al = both(sm.al[j][0]);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float4 k4 = *reinterpret_cast<const float4 *>(&sm.k[j][col0 + 32 * c]);
         const float4 q4 = *reinterpret_cast<const float4 *>(&sm.q[j][col0 + 32 * c]);
-        float4 a4 = make_float4(al0, al0, al0, al0);
+        float4 a4;
         if constexpr (PERCH) a4 = *reinterpret_cast<const float4 *>(&sm.al[j][col0 + 32 * c]);
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-          float *x = &s[i][4 * c];
-          x[0] *= a4.x; x[1] *= a4.y; x[2] *= a4.z; x[3] *= a4.w;  // decay first
-          part[i] += x[0] * k4.x + x[1] * k4.y + x[2] * k4.z + x[3] * k4.w;
-          part[RPT + i] += x[0] * q4.x + x[1] * q4.y + x[2] * q4.z + x[3] * q4.w;
+        for (int half = 0; half < 2; ++half) {
+          const float2 k2 = half ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+          const float2 q2 = half ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+          if constexpr (PERCH) al = half ? make_float2(a4.z, a4.w) : make_float2(a4.x, a4.y);
+#pragma unroll
+          for (int i = 0; i < RPT; ++i) {
+            float2 &x = s[i][2 * c + half];
+            x = mul2(x, al);  // decay first
+            p2[i] = fma2(x, k2, p2[i]);
+            r2[i] = fma2(x, q2, r2[i]);
+          }
         }
+      }
+      float part[NV];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        part[i] = p2[i].x + p2[i].y;
+        part[RPT + i] = r2[i].x + r2[i].y;
       }
       const float red = reduce8<NV>(part, lane);
       const float u_mine = sm.beta[j] * (v - red);  // meaningful where idx < RPT
@@ -203,49 +275,196 @@ __global__ void __launch_bounds__(kWarps * 32) gdr_step_slots_kernel(StepSlotsAr
       if (idx >= RPT && (lane & ((1 << SH) - 1)) == 0)
         store_out(a.o, to + row0 + 4 * mine, red + um * sm.kq[j], BF16);
       const int d = sm.dst[j];
-      float *out = a.pool + (size_t)max(d, 0) * a.slot_stride + in_slot;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float4 k4 = *reinterpret_cast<const float4 *>(&sm.k[j][col0 + 32 * c]);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-          float *x = &s[i][4 * c];
-          x[0] += u[i] * k4.x; x[1] += u[i] * k4.y; x[2] += u[i] * k4.z; x[3] += u[i] * k4.w;
-          if (d >= 0)
-            __stcs(reinterpret_cast<float4 *>(out + (size_t)i * 4 * DK + c * 32),
-                   make_float4(x[0], x[1], x[2], x[3]));
+          float2 &x = s[i][2 * c], &y = s[i][2 * c + 1];
+          x = fma2(both(u[i]), make_float2(k4.x, k4.y), x);
+          y = fma2(both(u[i]), make_float2(k4.z, k4.w), y);
         }
+      }
+      if (d >= 0) {
+        float *out = a.pool + (size_t)d * a.slot_stride + in_slot;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < RPT; ++i)
+            __stcs(reinterpret_cast<float4 *>(out + i * 4 * DK + c * 32),
+                   make_float4(s[i][2 * c].x, s[i][2 * c].y, s[i][2 * c + 1].x, s[i][2 * c + 1].y));
       }
     }
   }
 }
 
-template <int DK, int RPT>
-cudaError_t launch_rpt(const StepSlotsArgs &a, cudaStream_t stream) {
-  const size_t blocks = (size_t)a.R * a.H * (a.dv / (kWarps * 4 * RPT));
+// One token a request (a decode step): 8 rows a warp, lane l holding channels
+// [l DK / 32, (l + 1) DK / 32) of each, so that k, q and the gate are DK / 32
+// values a lane and every warp prepares them for itself: nothing is shared and
+// nothing waits at a barrier, and a warp's stores leave while others load.
+template <int DK, bool BF16, bool PERCH>
+__global__ void __launch_bounds__(128, 7) gdr_step_slots_one_kernel(StepSlotsArgs a) {
+  constexpr int VEC = DK / 32, kRows = 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int blocks_per_head = a.dv / (4 * kRows);
+  const unsigned rh = blockIdx.x / blocks_per_head;
+  const int r = rh / a.H, h = rh % a.H;
+  const int hk = h / (a.H / a.Hk);
+  const int row0 = (blockIdx.x % blocks_per_head) * 4 * kRows + warp * kRows;
+  const int src = a.src[r];
+  int dst = a.dst ? a.dst[r] : src;
+  const size_t th = rh;
+  // (requested before the slot is known)
+  float kv[VEC], qv[VEC], al[VEC];
+  load_lane<VEC, BF16>(a.k, (size_t)r * a.k_stride + (size_t)hk * DK + lane * VEC, kv);
+  load_lane<VEC, BF16>(a.q, (size_t)r * a.q_stride + (size_t)hk * DK + lane * VEC, qv);
+  if constexpr (PERCH)
+    load_lane<VEC, false>(a.g, th * DK + lane * VEC, al);
+  else
+    al[0] = a.g[th];
+  float beta = a.beta[th];
+  // v of row (lane / 2) % 8, as the sums come out below
+  const float v = load_in(a.v, (size_t)r * a.v_stride + (size_t)h * a.dv + row0 + ((lane >> 1) & 7), BF16);
+
+  if (src == GDR_SLOT_SKIP) return;
+  if (src < GDR_SLOT_ZERO || src >= a.slots) {
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusSlot);
+    return;
+  }
+  if (a.dst && (dst < -1 || dst >= a.slots)) {
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusSlot);
+    dst = -1;
+  }
+  const size_t in_slot = ((size_t)h * a.dv + row0) * DK + lane * VEC;
+  float s[kRows][VEC];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (src >= 0) {
+      load_lane_stream<VEC>(a.pool + (size_t)src * a.slot_stride + in_slot + i * DK, s[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s[i][e] = 0.f;
+    }
+  }
+
+  float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    kk += kv[e] * kv[e];
+    qq += qv[e] * qv[e];
+    kq += kv[e] * qv[e];
+  }
+  kq = warp_sum(kq);
+  if (a.norm_qk & GDR_NORM_K) {
+    const float f = rsqrtf(warp_sum(kk) + kNormEps);
+    kq *= f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) kv[e] *= f;
+  }
+  if (a.norm_qk & GDR_NORM_Q) {
+    const float f = rsqrtf(warp_sum(qq) + kNormEps);
+    kq *= f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) qv[e] *= f;
+  }
+  const float scale = a.gate_scale ? a.gate_scale[h] : 0.f;
+  if (a.gate_scale) beta = 1.f / (1.f + expf(-beta));
+#pragma unroll
+  for (int e = 0; e < (PERCH ? VEC : 1); ++e)
+    al[e] = expf(a.gate_scale ? -scale * softplus(al[e]) : al[e]);
+  if constexpr (!PERCH) {
+#pragma unroll
+    for (int e = 1; e < VEC; ++e) al[e] = al[0];
+  }
+
+  float part[16];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    float p = 0.f, o = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      s[i][e] *= al[e];  // decay first
+      p += s[i][e] * kv[e];
+      o += s[i][e] * qv[e];
+    }
+    part[i] = p;
+    part[8 + i] = o;
+  }
+  // Halving sums over the warp: lane l ends up with value l / 2 (p of row l / 2 below 8, else
+  // r of row l / 2 - 8).
+#pragma unroll
+  for (int m = 16, n = 8; n; m >>= 1, n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool hi = lane & m;
+      const float send = hi ? part[i] : part[i + n];
+      const float keep = hi ? part[i + n] : part[i];
+      part[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+    }
+  const float red = part[0] + __shfl_xor_sync(0xffffffffu, part[0], 1);
+  const float u_mine = beta * (v - red);  // meaningful on lanes < 16
+  const float u_row = __shfl_sync(0xffffffffu, u_mine, lane & 15);
+  if (lane >= 16 && !(lane & 1))
+    store_out(a.o, th * a.dv + row0 + ((lane >> 1) & 7), red + u_row * kq, BF16);
+  if (dst < 0) return;
+  float *out = a.pool + (size_t)dst * a.slot_stride + in_slot;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const float u = __shfl_sync(0xffffffffu, u_mine, 2 * i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[i][e] += u * kv[e];
+    store_lane_stream<VEC>(out + i * DK, s[i]);
+  }
+}
+
+template <int DK, int WARPS>
+cudaError_t launch_warps(const StepSlotsArgs &a, cudaStream_t stream) {
+  const size_t blocks = (size_t)a.R * a.H * (a.dv / rows_of(WARPS));
   if (blocks > 0x7fffffffu) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(kWarps * 32);
+  const dim3 grid((unsigned)blocks), block(WARPS * 32);
   if (a.bf16) {
     if (a.per_channel)
-      gdr_step_slots_kernel<DK, RPT, true, true><<<grid, block, 0, stream>>>(a);
+      gdr_step_slots_kernel<DK, WARPS, true, true><<<grid, block, 0, stream>>>(a);
     else
-      gdr_step_slots_kernel<DK, RPT, true, false><<<grid, block, 0, stream>>>(a);
+      gdr_step_slots_kernel<DK, WARPS, true, false><<<grid, block, 0, stream>>>(a);
   } else {
     if (a.per_channel)
-      gdr_step_slots_kernel<DK, RPT, false, true><<<grid, block, 0, stream>>>(a);
+      gdr_step_slots_kernel<DK, WARPS, false, true><<<grid, block, 0, stream>>>(a);
     else
-      gdr_step_slots_kernel<DK, RPT, false, false><<<grid, block, 0, stream>>>(a);
+      gdr_step_slots_kernel<DK, WARPS, false, false><<<grid, block, 0, stream>>>(a);
   }
   return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t launch_dk(const StepSlotsArgs &a, cudaStream_t stream) {
+  if (!a.cu) {
+    const size_t blocks = (size_t)a.R * a.H * (a.dv / 32);
+    if (blocks > 0x7fffffffu) return cudaErrorInvalidValue;
+    const unsigned n = (unsigned)blocks;
+    if (a.bf16) {
+      if (a.per_channel)
+        gdr_step_slots_one_kernel<DK, true, true><<<n, 128, 0, stream>>>(a);
+      else
+        gdr_step_slots_one_kernel<DK, true, false><<<n, 128, 0, stream>>>(a);
+    } else {
+      if (a.per_channel)
+        gdr_step_slots_one_kernel<DK, false, true><<<n, 128, 0, stream>>>(a);
+      else
+        gdr_step_slots_one_kernel<DK, false, false><<<n, 128, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+  }
+  return a.dv == 32 ? launch_warps<DK, 4>(a, stream) : launch_warps<DK, 8>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_step_slots(const StepSlotsArgs &a, cudaStream_t stream) {
   switch (a.dk) {
-    case 32: return launch_rpt<32, 2>(a, stream);
-    case 64: return launch_rpt<64, 2>(a, stream);
-    case 128: return launch_rpt<128, 2>(a, stream);
+    case 32: return launch_dk<32>(a, stream);
+    case 64: return launch_dk<64>(a, stream);
+    case 128: return launch_dk<128>(a, stream);
   }
   return cudaErrorInvalidValue;
 }
