@@ -27,10 +27,56 @@ inline int norm_vector(const GroupNormArgs &a) {
     const size_t bytes = (size_t)vec * size;
     if (a.D % vec == 0 && a.x_stride % vec == 0 && (!a.z || a.z_stride % vec == 0) &&
         multiple_of(a.x, bytes) && multiple_of(a.z, bytes) && multiple_of(a.dy, bytes) &&
-        multiple_of(a.y, bytes) && multiple_of(a.dz, bytes) && multiple_of(a.dx, 16))
+        multiple_of(a.y, bytes) && multiple_of(a.dz, bytes) && multiple_of(a.dx, 16) &&
+        multiple_of(a.weight, 16) && multiple_of(a.bias, 16))
       return vec;
   }
   return 1;
+}
+
+// Weights or biases of one access, as pairs (`none` where there are none).
+template <int VEC>
+__device__ __forceinline__ void load_affine(const float *p, int at, bool in, float none, float2 *x) {
+  float v[VEC + VEC % 2];
+#pragma unroll
+  for (int e = 0; e < VEC + VEC % 2; ++e) v[e] = none;
+  if (p && in) {
+    if constexpr (VEC >= 4) {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(p + at + e);
+        v[e] = t.x; v[e + 1] = t.y; v[e + 2] = t.z; v[e + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = p[at + e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) x[e / 2] = make_float2(v[e], v[e + 1]);
+}
+
+// Subtracts the group's mean from x (with center; what lies outside the group
+// stays 0) and returns 1 / sqrt(mean square + eps).
+template <int VEC, int L, int NV>
+__device__ __forceinline__ float normalise(float2 (&x)[(VEC + 1) / 2 * NV], const bool (&in)[NV],
+                                           int center, float inv_d, float eps) {
+  constexpr int H = (VEC + 1) / 2, N = H * NV;
+  if (center) {
+    float2 sum = both(0.f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum = add2(sum, x[e]);
+    const float m = lanes_sum<L>(sum.x + sum.y) * inv_d;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      x[e].x = in[e / H] ? x[e].x - m : 0.f;
+      x[e].y = in[e / H] && VEC > 1 ? x[e].y - m : 0.f;
+    }
+  }
+  float2 ss = both(0.f);
+#pragma unroll
+  for (int e = 0; e < N; ++e) ss = fma2(x[e], x[e], ss);
+  return rsqrtf(lanes_sum<L>(ss.x + ss.y) * inv_d + eps);
 }
 
 // Calls f.template operator()<T, VEC, L, NV>() for the layout of these

@@ -15,52 +15,81 @@ namespace {
 constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
 constexpr int blocks_per_sm(int E) { return E <= 8 ? 2 : 1; }
 
-// Value and slope of the activation.
-__device__ __forceinline__ void act_both(int act, float u, float &f, float &df) {
-  if (act == GDR_ACT_NONE) {
-    f = u;
-    df = 1.f;
-    return;
+// N pairs of a row.  On return x holds n and z dz; h, the running dw and db are
+// set, and the lane's part of sum(h n) is returned.  (dy is 0 outside the group and
+// behind the last row: so is all that is added up.)
+template <int ACT, bool GATED, int N>
+__device__ __forceinline__ float gradients(float2 (&x)[N], float2 (&z)[N], const float2 (&dy)[N],
+                                           const float2 (&w)[N], const float2 (&b)[N], float rstd,
+                                           float2 (&h)[N], float2 (&dw)[N], float2 (&db)[N]) {
+  float2 hn = both(0.f);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float2 n = mul2(x[e], both(rstd));
+    const float2 l = fma2(n, w[e], b[e]);
+    const float2 u = GATED ? z[e] : l;
+    float2 f = u, df = both(1.f);  // value and slope of the activation
+    if constexpr (ACT != GDR_ACT_NONE) {
+      const float2 s = sigmoid2(u), t = fma2(s, both(-1.f), both(1.f));
+      if constexpr (ACT == GDR_ACT_SILU) {
+        f = mul2(u, s);
+        df = fma2(f, t, s);
+      } else {
+        f = s;
+        df = mul2(s, t);
+      }
+    }
+    const float2 dl = mul2(dy[e], GATED ? f : df);
+    if constexpr (GATED) z[e] = mul2(mul2(dy[e], l), df);
+    dw[e] = fma2(dl, n, dw[e]);
+    db[e] = add2(db[e], dl);
+    h[e] = mul2(dl, w[e]);
+    hn = fma2(h[e], n, hn);
+    x[e] = n;
   }
-  const float s = sigmoid(u);
-  if (act == GDR_ACT_SILU) {
-    f = u * s;
-    df = s + f * (1.f - s);
-  } else {
-    f = s;
-    df = s * (1.f - s);
-  }
+  return hn.x + hn.y;
 }
 
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_bwd_kernel(GroupNormArgs a, RowPlan p) {
   constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
-  constexpr bool kAhead = E <= 16;  // (wider rows have no registers for a second one)
+  constexpr int H = (VEC + 1) / 2, N = H * NV;  // pairs of an access and of a lane
+  constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
+  constexpr bool kAhead = !kQueue && E <= 16;  // (wider rows have no registers for a second one)
   constexpr int kPerBlock = kRowThreads / L;
   const int lane = threadIdx.x % L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
   const float inv_d = 1.f / (float)a.D;
-  float w[E], b[E], dw[E], db[E];
+  float2 w[N], b[N], dw[N], db[N];
   bool in[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * L + lane) * VEC;
     in[i] = c < a.D;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int at = (a.per_channel ? g * a.D : 0) + c + e;
-      w[i * VEC + e] = a.weight && in[i] ? a.weight[at] : 1.f;
-      b[i * VEC + e] = a.bias && in[i] ? a.bias[at] : 0.f;
-      dw[i * VEC + e] = db[i * VEC + e] = 0.f;
-    }
+    load_affine<VEC>(a.weight, (a.per_channel ? g * a.D : 0) + c, in[i], 1.f, &w[i * H]);
+    load_affine<VEC>(a.bias, (a.per_channel ? g * a.D : 0) + c, in[i], 0.f, &b[i * H]);
   }
+#pragma unroll
+  for (int e = 0; e < N; ++e) dw[e] = db[e] = both(0.f);
   const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
   const long long off = (long long)g * a.D + lane * VEC, dense = (long long)a.G * a.D;
   const T *xp = static_cast<const T *>(a.x) + off, *zp = static_cast<const T *>(a.z) + off;
   const T *dyp = static_cast<const T *>(a.dy) + off;
   const long long turns = (a.rows + U * p.step - 1) / (U * p.step);
   long long row = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
+  // 16-byte accesses wait in shared memory, 3 rows of them; others a turn ahead in registers.
+  constexpr int kStages = 3;
+  __shared__ uint4 waiting[kQueue ? kStages : 1][3][kRowThreads];
+  Queue<3, kStages> queue{waiting};
+  const auto ask = [&](long long at, int stage) {
+    if (at < last && in[0]) {
+      queue.request(stage, 0, xp + at * a.x_stride);
+      if (a.z) queue.request(stage, 1, zp + at * a.z_stride);
+      queue.request(stage, 2, dyp + at * dense);
+    }
+    queue.commit();
+  };
   Raw<T, VEC> xn[U][NV], zn[U][NV], dyn[U][NV];  // the next turn's rows
   const auto request = [&](long long from) {
 #pragma unroll
@@ -77,76 +106,85 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
       }
   };
   if constexpr (kAhead) request(row);
+  if constexpr (kQueue) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ask(row + i * p.step, i);
+  }
+  int stage = 0;
   for (long long k = 0; k < turns; ++k) {
-    if constexpr (!kAhead) request(row);
     Raw<T, VEC> xr[U][NV], zr[U][NV], dyr[U][NV];
+    if constexpr (kQueue) {
+      ask(row + (kStages - 1) * p.step, stage == 0 ? kStages - 1 : stage - 1);
+      queue.wait();
+      const bool live = row < last && in[0];
+      const uint4 x16 = live ? queue.get(stage, 0) : uint4{};
+      const uint4 z16 = live && a.z ? queue.get(stage, 1) : uint4{};
+      const uint4 dy16 = live ? queue.get(stage, 2) : uint4{};
+      xr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&x16);
+      zr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&z16);
+      dyr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&dy16);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      if constexpr (!kAhead) request(row);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        xr[u][i] = xn[u][i];
-        zr[u][i] = zn[u][i];
-        dyr[u][i] = dyn[u][i];
-      }
-    if constexpr (kAhead) request(row + U * p.step);
+        for (int i = 0; i < NV; ++i) {
+          xr[u][i] = xn[u][i];
+          zr[u][i] = zn[u][i];
+          dyr[u][i] = dyn[u][i];
+        }
+      if constexpr (kAhead) request(row + U * p.step);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u, row += p.step) {
-      float x[E], m = 0.f, ss = 0.f;
+      float2 x[N], z[N], dy[N], h[N];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) unpack<T, VEC>(xr[u][i], &x[i * VEC]);
-      if (a.center) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) m += x[e];
-        m = lanes_sum<L>(m) * inv_d;
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = x[i * VEC + e] - m;
-          x[i * VEC + e] = d;
-          ss += in[i] ? d * d : 0.f;
-        }
-      const float rstd = rsqrtf(lanes_sum<L>(ss) * inv_d + a.eps);
-      float h[E], sh = 0.f, shn = 0.f;
+      for (int i = 0; i < NV; ++i) unpack2<T, VEC>(xr[u][i], &x[i * H]);
+      const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float z[VEC], dy[VEC], dz[VEC];
-        unpack<T, VEC>(zr[u][i], z);
-        unpack<T, VEC>(dyr[u][i], dy);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int j = i * VEC + e;
-          const float n = x[j] * rstd;
-          const float l = n * w[j] + b[j];
-          float f, df;
-          act_both(a.act, a.z ? z[e] : l, f, df);
-          const float dl = dy[e] * (a.z ? f : df);
-          dz[e] = dy[e] * l * df;
-          // (dy is zero outside the group and the rows: so are all of these)
-          dw[j] += dl * n;
-          db[j] += dl;
-          h[j] = dl * w[j];
-          x[j] = n;
-          sh += h[j];
-          shn += h[j] * n;
-        }
-        if (a.dz && row < last && in[i])
-          store_vec<T, VEC>(static_cast<T *>(a.dz) + off + row * dense + i * L * VEC, dz);
+        unpack2<T, VEC>(zr[u][i], &z[i * H]);
+        unpack2<T, VEC>(dyr[u][i], &dy[i * H]);
       }
-      shn = lanes_sum<L>(shn) * inv_d;
-      sh = a.center ? lanes_sum<L>(sh) * inv_d : 0.f;
+      float hn;
+      if (a.z) {
+        if (a.act == GDR_ACT_SILU)
+          hn = gradients<GDR_ACT_SILU, true>(x, z, dy, w, b, rstd, h, dw, db);
+        else if (a.act == GDR_ACT_SIGMOID)
+          hn = gradients<GDR_ACT_SIGMOID, true>(x, z, dy, w, b, rstd, h, dw, db);
+        else
+          hn = gradients<GDR_ACT_NONE, true>(x, z, dy, w, b, rstd, h, dw, db);
+      } else {
+        if (a.act == GDR_ACT_SILU)
+          hn = gradients<GDR_ACT_SILU, false>(x, z, dy, w, b, rstd, h, dw, db);
+        else if (a.act == GDR_ACT_SIGMOID)
+          hn = gradients<GDR_ACT_SIGMOID, false>(x, z, dy, w, b, rstd, h, dw, db);
+        else
+          hn = gradients<GDR_ACT_NONE, false>(x, z, dy, w, b, rstd, h, dw, db);
+      }
+      hn = lanes_sum<L>(hn) * inv_d;
+      float mean = 0.f;  // of h
+      if (a.center) {
+        float2 sum = both(0.f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum = add2(sum, h[e]);
+        mean = lanes_sum<L>(sum.x + sum.y) * inv_d;
+      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (row >= last || !in[i]) continue;
-        float d[VEC];
+        const long long at = off + row * dense + i * L * VEC;
+        if (a.dz) store_vec2<T, VEC>(static_cast<T *>(a.dz) + at, &z[i * H]);
+        float2 d[H];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          d[e] = rstd * (h[i * VEC + e] - sh - x[i * VEC + e] * shn);
+        for (int e = 0; e < H; ++e) {  // rstd h - rstd mean - n (rstd hn)
+          const float2 n = x[i * H + e];
+          d[e] = fma2(h[i * H + e], both(rstd), fma2(n, both(-rstd * hn), both(-rstd * mean)));
+        }
         constexpr int V4 = VEC < 4 ? VEC : 4;
 #pragma unroll
-        for (int e = 0; e < VEC; e += V4)
-          store_vec<float, V4>(a.dx + off + row * dense + i * L * VEC + e, d + e);
+        for (int e = 0; e < VEC; e += V4) store_vec2<float, V4>(a.dx + at + e, d + e / 2);
       }
     }
   }
@@ -165,7 +203,8 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      float v = which ? db[e] : dw[e];
+      const float2 sums = (which ? db : dw)[e / VEC * H + e % VEC / 2];
+      float v = e % VEC % 2 ? sums.y : sums.x;
 #pragma unroll
       for (int m = L; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
       // (element e of a lane is channel ((e / VEC) L + lane) VEC + e % VEC)
@@ -189,14 +228,15 @@ __global__ void __launch_bounds__(1024) group_norm_sum_kernel(const float *part,
     sum_columns(part + (blockIdx.y ? (size_t)rows * cols : 0), rows, cols, out, blockIdx.x);
 }
 
+constexpr int kTurns = 16;
 constexpr int kFewTurns = 4;  // rows a slot takes rather than have a second launch
 
 RowPlan bwd_plan(long long rows, int G, int lanes, int per_sm, int per_channel) {
   const int per_block = kRowThreads / lanes;
-  RowPlan p = row_plan(rows, G, per_block, kSMs * per_sm, per_channel);
+  RowPlan p = row_plan(rows, G, per_block, kTurns, kSMs * per_sm, per_channel);
   // few rows: as few blocks as have every channel once
   if (per_channel ? rows <= kFewTurns * per_block : rows * G <= kFewTurns * per_block)
-    p = row_plan(rows, G, per_block, per_channel ? G : 1, per_channel);
+    p = row_plan(rows, G, per_block, kFewTurns, 1, per_channel);
   p.sum = p.blocks > (per_channel ? G : 1);
   return p;
 }

@@ -9,33 +9,42 @@ namespace {
 constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
 constexpr int blocks_per_sm(int E) { return E <= 8 ? 4 : E <= 16 ? 2 : 1; }
 
-__device__ __forceinline__ float act_of(int act, float u) {
-  if (act == GDR_ACT_NONE) return u;
-  const float s = sigmoid(u);
-  return act == GDR_ACT_SILU ? u * s : s;
+constexpr int kTurns = 8;
+
+// y of N pairs in place of x: x are normalised but for rstd.
+template <int ACT, bool GATED, int N>
+__device__ __forceinline__ void finish(float2 (&x)[N], const float2 (&z)[N], const float2 (&w)[N],
+                                       const float2 (&b)[N], float rstd) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float2 l = fma2(mul2(x[e], both(rstd)), w[e], b[e]);
+    const float2 u = GATED ? z[e] : l;
+    float2 f = u;
+    if constexpr (ACT != GDR_ACT_NONE) f = sigmoid2(u);
+    if constexpr (ACT == GDR_ACT_SILU) f = mul2(f, u);
+    x[e] = GATED ? mul2(f, l) : f;
+  }
 }
 
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_fwd_kernel(GroupNormArgs a, RowPlan p) {
   constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
-  constexpr bool kAhead = E <= 16;  // (wider rows have no registers for a second one)
+  constexpr int H = (VEC + 1) / 2, N = H * NV;  // pairs of an access and of a lane
+  constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
+  constexpr bool kAhead = !kQueue && E <= 16;  // (wider rows have no registers for a second one)
   const int lane = threadIdx.x % L;
   constexpr int kPerBlock = kRowThreads / L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
   const float inv_d = 1.f / (float)a.D;
-  float w[E], b[E];
+  float2 w[N], b[N];
   bool in[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * L + lane) * VEC;
     in[i] = c < a.D;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int at = (a.per_channel ? g * a.D : 0) + c + e;
-      w[i * VEC + e] = a.weight && in[i] ? a.weight[at] : 1.f;
-      b[i * VEC + e] = a.bias && in[i] ? a.bias[at] : 0.f;
-    }
+    load_affine<VEC>(a.weight, (a.per_channel ? g * a.D : 0) + c, in[i], 1.f, &w[i * H]);
+    load_affine<VEC>(a.bias, (a.per_channel ? g * a.D : 0) + c, in[i], 0.f, &b[i * H]);
   }
   // (all lanes of a warp take every turn: the sums shuffle over whole warps)
   const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
@@ -44,6 +53,17 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   T *yp = static_cast<T *>(a.y) + (long long)g * a.D + lane * VEC;
   const long long turns = (a.rows + U * p.step - 1) / (U * p.step);
   long long row = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
+  // 16-byte accesses wait in shared memory, 4 rows of them; others a turn ahead in registers.
+  constexpr int kStages = 4;
+  __shared__ uint4 waiting[kQueue ? kStages : 1][2][kRowThreads];
+  Queue<2, kStages> queue{waiting};
+  const auto ask = [&](long long at, int stage) {
+    if (at < last && in[0]) {
+      queue.request(stage, 0, xp + at * a.x_stride);
+      if (a.z) queue.request(stage, 1, zp + at * a.z_stride);
+    }
+    queue.commit();
+  };
   Raw<T, VEC> xn[U][NV], zn[U][NV];  // the next turn's rows
   const auto request = [&](long long from) {
 #pragma unroll
@@ -59,48 +79,55 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
       }
   };
   if constexpr (kAhead) request(row);
+  if constexpr (kQueue) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ask(row + i * p.step, i);
+  }
+  int stage = 0;
   for (long long k = 0; k < turns; ++k) {
-    if constexpr (!kAhead) request(row);
     Raw<T, VEC> xr[U][NV], zr[U][NV];
+    if constexpr (kQueue) {
+      ask(row + (kStages - 1) * p.step, stage == 0 ? kStages - 1 : stage - 1);
+      queue.wait();
+      const bool live = row < last && in[0];
+      const uint4 x16 = live ? queue.get(stage, 0) : uint4{};
+      const uint4 z16 = live && a.z ? queue.get(stage, 1) : uint4{};
+      xr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&x16);
+      zr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&z16);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      if constexpr (!kAhead) request(row);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        xr[u][i] = xn[u][i];
-        zr[u][i] = zn[u][i];
-      }
-    if constexpr (kAhead) request(row + U * p.step);
+        for (int i = 0; i < NV; ++i) {
+          xr[u][i] = xn[u][i];
+          zr[u][i] = zn[u][i];
+        }
+      if constexpr (kAhead) request(row + U * p.step);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u, row += p.step) {
-      float x[E], m = 0.f, ss = 0.f;
+      float2 x[N], z[N];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) unpack<T, VEC>(xr[u][i], &x[i * VEC]);
-      if (a.center) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) m += x[e];
-        m = lanes_sum<L>(m) * inv_d;
+      for (int i = 0; i < NV; ++i) {
+        unpack2<T, VEC>(xr[u][i], &x[i * H]);
+        unpack2<T, VEC>(zr[u][i], &z[i * H]);
+      }
+      const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
+      if (a.z) {
+        if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, true>(x, z, w, b, rstd);
+        else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, true>(x, z, w, b, rstd);
+        else finish<GDR_ACT_NONE, true>(x, z, w, b, rstd);
+      } else {
+        if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, false>(x, z, w, b, rstd);
+        else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, false>(x, z, w, b, rstd);
+        else finish<GDR_ACT_NONE, false>(x, z, w, b, rstd);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = x[i * VEC + e] - m;
-          x[i * VEC + e] = d;
-          ss += in[i] ? d * d : 0.f;
-        }
-      const float rstd = rsqrtf(lanes_sum<L>(ss) * inv_d + a.eps);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (row >= last || !in[i]) continue;
-        float z[VEC], y[VEC];
-        unpack<T, VEC>(zr[u][i], z);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float l = x[i * VEC + e] * rstd * w[i * VEC + e] + b[i * VEC + e];
-          y[e] = a.z ? act_of(a.act, z[e]) * l : act_of(a.act, l);
-        }
-        store_vec<T, VEC>(yp + row * a.G * a.D + i * L * VEC, y);
-      }
+        if (row < last && in[i])
+          store_vec2<T, VEC>(yp + row * a.G * a.D + i * L * VEC, &x[i * H]);
     }
   }
 }
@@ -111,7 +138,7 @@ struct Launch {
   template <typename T, int VEC, int L, int NV>
   cudaError_t operator()() const {
     const RowPlan p =
-        row_plan(a.rows, a.G, kRowThreads / L, kSMs * blocks_per_sm(VEC * NV), false);
+        row_plan(a.rows, a.G, kRowThreads / L, kTurns, kSMs * blocks_per_sm(VEC * NV), false);
     group_norm_fwd_kernel<T, VEC, L, NV><<<p.blocks, kRowThreads, 0, stream>>>(a, p);
     return cudaGetLastError();
   }

@@ -21,7 +21,8 @@ namespace gdr {
 namespace {
 
 constexpr float kNormEps = 1e-6f;
-constexpr int kNormBlocks = 4 * kSMs, kGateBlocks = 8 * kSMs;  // at most
+constexpr int kNormTurns = 4, kNormBlocks = 4 * kSMs;
+constexpr int kGateBlocks = 8 * kSMs;  // at most
 
 // The gates' blocks: `heads` heads of `tokens` tokens at a time; blocks that
 // share a tile of heads are `step` tokens apart.
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(1024) prologue_sum_kernel(const float *part, i
 
 template <bool BWD, typename T, int VEC, int L>
 cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
-  const Split p = {row_plan(a.tokens, a.Hk, kRowThreads / L, kNormBlocks, false),
+  const Split p = {row_plan(a.tokens, a.Hk, kRowThreads / L, kNormTurns, kNormBlocks, false),
                    gate_plan(a.tokens, a.H, a.d, a.per_channel)};
   const int blocks = p.norm.blocks + p.gate.blocks;
   if constexpr (!BWD) {

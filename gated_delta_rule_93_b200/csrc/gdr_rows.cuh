@@ -22,30 +22,36 @@ struct RowPlan {
   long long step;
 
   __device__ __forceinline__ int group(int block, int slot_in_block, int per_block, int G) const {
-    return by_block ? block % G : (block * per_block + slot_in_block) % G;
+    return (unsigned)(by_block ? block : block * per_block + slot_in_block) % (unsigned)G;
   }
   __device__ __forceinline__ long long first_row(int block, int slot_in_block, int per_block,
                                                  int G) const {
-    return by_block ? (long long)(block / G) * per_block + slot_in_block
-                    : (block * per_block + slot_in_block) / G;
+    const unsigned q = (unsigned)(by_block ? block : block * per_block + slot_in_block) / (unsigned)G;
+    return by_block ? (long long)q * per_block + slot_in_block : q;
   }
   __device__ __forceinline__ bool used(int block, int slot_in_block, int per_block) const {
     return by_block || block * per_block + slot_in_block < slots;
   }
 };
 
-inline RowPlan row_plan(long long rows, int G, int per_block, int max_blocks, bool by_block) {
-  const long long least = by_block ? G : ((long long)G + per_block - 1) / per_block;
-  long long blocks = by_block ? (rows + per_block - 1) / per_block * G
-                              : (rows * G + per_block - 1) / per_block;
-  if (blocks > max_blocks) blocks = by_block ? max_blocks / G * G : max_blocks;
-  if (blocks < least) blocks = least;  // every group once
+// A plan in which a slot takes about `turns` rows, and at least `least_blocks`
+// blocks share the work where there is enough of it.
+inline RowPlan row_plan(long long rows, int G, int per_block, int turns, int least_blocks,
+                        bool by_block) {
+  const long long whole = by_block ? (rows + per_block - 1) / per_block * G
+                                   : (rows * G + per_block - 1) / per_block;  // a row a slot
+  const long long every = by_block ? G : ((long long)G + per_block - 1) / per_block;
+  long long blocks = (whole + turns - 1) / turns;
+  if (blocks < least_blocks) blocks = whole < least_blocks ? whole : least_blocks;
+  if (by_block) blocks = (blocks + G - 1) / G * G;
+  if (blocks < every) blocks = every;  // every group once
+  if (blocks > 1 << 24) blocks = by_block ? (1 << 24) / G * G : 1 << 24;  // (32-bit slots)
   RowPlan p;
   p.blocks = (int)blocks;
   p.by_block = by_block;
   p.sum = 0;
   p.step = by_block ? blocks / G * per_block : blocks * per_block / G;
-  p.slots = (int)(by_block ? blocks * per_block : p.step * G);
+  p.slots = by_block ? 0 : (int)(p.step * G);
   return p;
 }
 
@@ -82,9 +88,31 @@ __device__ __forceinline__ void unpack(const Raw<T, VEC> &raw, float *x) {
   for (int e = 0; e < VEC; ++e) x[e] = to_f(u.t[e]);
 }
 
+// The same as pairs (a single element is the first of a pair with 0).
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack2(const Raw<T, VEC> &raw, float2 *x) {
+  float v[VEC + VEC % 2] = {};
+  unpack<T, VEC>(raw, v);
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) x[e / 2] = make_float2(v[e], v[e + 1]);
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T *p, float *x) {
   unpack<T, VEC>(load_raw<T, VEC>(p), x);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T *p, const float *x);
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec2(T *p, const float2 *x) {
+  float v[VEC + VEC % 2];
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) {
+    v[e] = x[e / 2].x;
+    v[e + 1] = x[e / 2].y;
+  }
+  store_vec<T, VEC>(p, v);
 }
 
 template <typename T, int VEC>
@@ -98,6 +126,28 @@ __device__ __forceinline__ void store_vec(T *p, const float *x) {
   *reinterpret_cast<Raw<T, VEC> *>(p) = u.b;
 }
 
+// A thread's own queue of 16-byte loads in shared memory, STAGES rows of TENSORS
+// accesses: more bytes in flight than registers have room for.  Only the thread
+// that asked for them reads them, so nothing waits at a barrier.
+template <int TENSORS, int STAGES>
+struct Queue {
+  uint4 (*buf)[TENSORS][kRowThreads];  // [STAGES] in shared memory
+
+  __device__ __forceinline__ void request(int stage, int tensor, const void *p) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&buf[stage][tensor][threadIdx.x]);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+  }
+  // Ends a row's requests (also of a row that has none).
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Waits for all rows but the last STAGES - 1 that were asked for.
+  __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+  }
+  __device__ __forceinline__ uint4 get(int stage, int tensor) const {
+    return buf[stage][tensor][threadIdx.x];
+  }
+};
+
 // The sum over the L lanes (a power of two) that share a row, in all of them.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float x) {
@@ -106,9 +156,45 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
+// Two fp32 values in one register pair, worked on by one instruction.
+__device__ __forceinline__ unsigned long long bits(float2 x) {
+  return *reinterpret_cast<unsigned long long *>(&x);
+}
+__device__ __forceinline__ float2 pair(unsigned long long x) {
+  return *reinterpret_cast<float2 *>(&x);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Fast exponential and reciprocal: relative error below (4 + |x|) 2^-23, a few
 // instructions instead of about thirty.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Both halves: the negated argument is scaled to a power of two in one instruction.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 t = mul2(x, both(-1.4426950408889634f));  // -log2(e)
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, both(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+  return e;
+}
 
 // log(1 + e^x), with no branch that overflows, and 1 / (1 + e^-x) from the same exponential.
 __device__ __forceinline__ float softplus(float x, float *sig = nullptr) {
@@ -118,10 +204,10 @@ __device__ __forceinline__ float softplus(float x, float *sig = nullptr) {
 }
 
 // out[c] = sum over k of part[k * cols + c], in a fixed order.  A block of 1024
-// threads takes W columns (a power of two up to 32, fewer where there are
-// few columns, so that more threads share one) and adds up in a tree.
+// threads takes W columns (32 bytes of a row, or 16 of a short one) and adds up
+// in a tree.
 __host__ __device__ __forceinline__ int sum_width(int cols) {
-  return cols <= 4 ? 4 : cols <= 8 ? 8 : cols <= 16 ? 16 : 32;
+  return cols <= 4 ? 4 : 8;
 }
 __device__ __forceinline__ void sum_columns(const float *part, int rows, int cols, float *out,
                                             int block) {

@@ -17,24 +17,26 @@
 // products need 3 shuffle steps instead of 5.  What all rows of a head share (k, q
 // with their norms, the gates, k . q) is prepared once per block in shared
 // memory, 8 tokens at a time, a warp each: the first 8 while the state's loads are in flight.
-#include "gdr_internal.cuh"
+#include "gdr_rows.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kRpt = 2;  // rows per thread, 4 threads apart
-constexpr int rows_of(int warps) { return 4 * kRpt * warps; }  // of a block
+constexpr int kRpt = 4;                 // rows per thread, 4 apart
+constexpr int kWarpRows = 4 * kRpt;      // rows of a warp
+constexpr int kTokens = 8;               // tokens prepared at a time
+constexpr int rows_of(int warps) { return kWarpRows * warps; }  // of a block
 
 constexpr float kNormEps = 1e-6f;
 
 template <int DK, int WARPS, bool PERCH>
-struct __align__(16) Prepared {  // a token a warp
-  float k[WARPS][DK];
-  float q[WARPS][DK];
-  float al[WARPS][PERCH ? DK : 4];
-  float v[WARPS][rows_of(WARPS)];
-  float beta[WARPS], kq[WARPS];
-  int dst[WARPS];
+struct __align__(16) Prepared {
+  float k[kTokens][DK];
+  float q[kTokens][DK];
+  float al[kTokens][PERCH ? DK : 4];
+  float v[kTokens][rows_of(WARPS)];
+  float beta[kTokens], kq[kTokens];
+  int dst[kTokens];
 };
 
 // VEC consecutive values of a lane: q, k, v or a gate, and the state's (read once).
@@ -74,35 +76,11 @@ __device__ __forceinline__ void store_lane_stream(float *p, const float (&x)[VEC
     __stcs(p, x[0]);
 }
 
-// log(1 + e^x), with no branch that overflows.
-__device__ __forceinline__ float softplus(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-}
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
   return x;
 }
-
-// Two fp32 products or multiply-adds in one instruction.
-__device__ __forceinline__ unsigned long long bits(float2 x) {
-  return *reinterpret_cast<unsigned long long *>(&x);
-}
-__device__ __forceinline__ float2 pair(unsigned long long x) {
-  return *reinterpret_cast<float2 *>(&x);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-  return pair(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return pair(d);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Sum NV per-lane values over groups of 8 lanes, halving the values while the
 // lane masks allow it: afterwards a lane holds the sum of value (lane & 7) >> SH,
@@ -132,20 +110,17 @@ __device__ __forceinline__ float reduce8(float (&x)[NV], int lane) {
 }
 
 template <int DK, int WARPS, bool BF16, bool PERCH>
-__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(StepSlotsArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 32) / WARPS)
+    gdr_step_slots_kernel(StepSlotsArgs a) {
   constexpr int RPT = kRpt, kRows = rows_of(WARPS);
   constexpr int NC = DK / 32;  // float4s of a row per lane
   constexpr int NV = 2 * RPT;  // dot products per thread
   constexpr int SH = NV == 8 ? 0 : NV == 4 ? 1 : 2;
   __shared__ Prepared<DK, WARPS, PERCH> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int blocks_per_head = a.dv / kRows;
-  const unsigned rh = blockIdx.x / blocks_per_head;
-  const int r = rh / a.H, h = rh % a.H;
+  const int r = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int hk = h / (a.H / a.Hk);
-  const int block_row = (blockIdx.x % blocks_per_head) * kRows;
-  const int in_block = warp * 4 * RPT + (lane >> 3);  // this thread's rows: in_block + 4 i
-  const int row0 = block_row + in_block;
+  const int row0 = warp * kWarpRows + (lane >> 3);  // this thread's rows: row0 + 4 i
   const int col0 = (lane & 7) * 4;
 
   int t0 = r, t1 = r + 1;
@@ -179,11 +154,11 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(
       for (int c = 0; c < 2 * NC; ++c) s[i][c] = make_float2(0.f, 0.f);
   }
 
-  for (int tb = t0; tb < t1; tb += WARPS) {
-    const int n = min(WARPS, t1 - tb);
+  for (int tb = t0; tb < t1; tb += kTokens) {
+    const int n = min(kTokens, t1 - tb);
     if (tb != t0) __syncthreads();
-    if (warp < n) {  // warp w prepares token tb + w, DK / 32 channels and some values a lane
-      const size_t t = tb + warp, th = t * a.H + h;
+    for (int j = warp; j < n; j += WARPS) {  // a token a warp, DK / 32 channels a lane
+      const size_t t = tb + j, th = t * a.H + h;
       float kv[NC], qv[NC], gv[PERCH ? NC : 1];
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
@@ -197,8 +172,8 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(
       int d = a.dst ? a.dst[t] : ((int)t == t1 - 1 ? src : -1);
 #pragma unroll
       for (int e = 0; e < kRows / 32; ++e)
-        sm.v[warp][lane + 32 * e] =
-            load_in(a.v, t * a.v_stride + (size_t)h * a.dv + block_row + lane + 32 * e, BF16);
+        sm.v[j][lane + 32 * e] =
+            load_in(a.v, t * a.v_stride + (size_t)h * a.dv + lane + 32 * e, BF16);
       const float scale = a.gate_scale ? a.gate_scale[h] : 0.f;
       float kk = 0.f, qq = 0.f, kq = 0.f, rk = 1.f, rq = 1.f;
 #pragma unroll
@@ -212,21 +187,21 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(
       if (a.norm_qk & GDR_NORM_Q) rq = rsqrtf(warp_sum(qq) + kNormEps);
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        sm.k[warp][lane + 32 * e] = kv[e] * rk;
-        sm.q[warp][lane + 32 * e] = qv[e] * rq;
+        sm.k[j][lane + 32 * e] = kv[e] * rk;
+        sm.q[j][lane + 32 * e] = qv[e] * rq;
         if constexpr (PERCH)
-          sm.al[warp][lane + 32 * e] = expf(a.gate_scale ? -scale * softplus(gv[e]) : gv[e]);
+          sm.al[j][lane + 32 * e] = expf(a.gate_scale ? -scale * softplus(gv[e]) : gv[e]);
       }
       if (lane == 0) {
         if constexpr (!PERCH)
-          sm.al[warp][0] = expf(a.gate_scale ? -scale * softplus(gv[0]) : gv[0]);
-        sm.beta[warp] = a.gate_scale ? 1.f / (1.f + expf(-bl)) : bl;
-        sm.kq[warp] = kq * rk * rq;
+          sm.al[j][0] = expf(a.gate_scale ? -scale * softplus(gv[0]) : gv[0]);
+        sm.beta[j] = a.gate_scale ? sigmoid(bl) : bl;
+        sm.kq[j] = kq * rk * rq;
         if (d >= a.slots || d < -1) {
           atomicOr(a.status, kStatusSlot);
           d = -1;
         }
-        sm.dst[warp] = d;
+        sm.dst[j] = d;
       }
     }
     __syncthreads();
@@ -234,8 +209,8 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(
       const size_t to = ((size_t)(tb + j) * a.H + h) * a.dv;
       const int idx = (lane & 7) >> SH;   // the dot product this lane ends up with
       const int mine = idx % RPT;         // its row: p for idx < RPT, r after
-      const float v = sm.v[j][in_block + 4 * mine];
-      float2 p2[RPT] = {}, r2[RPT] = {};
+      const float v = sm.v[j][row0 + 4 * mine];
+      float2 p2[RPT] = {}, r2[RPT] = {}, kr[2 * NC];
       float2 al = both(0.f);
       if constexpr (!PERCH) al = both(sm.al[j][0]);
 #pragma unroll
@@ -247,6 +222,7 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const float2 k2 = half ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+          kr[2 * c + half] = k2;
           const float2 q2 = half ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
           if constexpr (PERCH) al = half ? make_float2(a4.z, a4.w) : make_float2(a4.x, a4.y);
 #pragma unroll
@@ -276,15 +252,9 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gdr_step_slots_kernel(
         store_out(a.o, to + row0 + 4 * mine, red + um * sm.kq[j], BF16);
       const int d = sm.dst[j];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float4 k4 = *reinterpret_cast<const float4 *>(&sm.k[j][col0 + 32 * c]);
+      for (int c = 0; c < 2 * NC; ++c)
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-          float2 &x = s[i][2 * c], &y = s[i][2 * c + 1];
-          x = fma2(both(u[i]), make_float2(k4.x, k4.y), x);
-          y = fma2(both(u[i]), make_float2(k4.z, k4.w), y);
-        }
-      }
+        for (int i = 0; i < RPT; ++i) s[i][c] = fma2(both(u[i]), kr[c], s[i][c]);
       if (d >= 0) {
         float *out = a.pool + (size_t)d * a.slot_stride + in_slot;
 #pragma unroll
@@ -368,7 +338,7 @@ __global__ void __launch_bounds__(128, 7) gdr_step_slots_one_kernel(StepSlotsArg
     for (int e = 0; e < VEC; ++e) qv[e] *= f;
   }
   const float scale = a.gate_scale ? a.gate_scale[h] : 0.f;
-  if (a.gate_scale) beta = 1.f / (1.f + expf(-beta));
+  if (a.gate_scale) beta = sigmoid(beta);
 #pragma unroll
   for (int e = 0; e < (PERCH ? VEC : 1); ++e)
     al[e] = expf(a.gate_scale ? -scale * softplus(al[e]) : al[e]);
@@ -419,7 +389,7 @@ __global__ void __launch_bounds__(128, 7) gdr_step_slots_one_kernel(StepSlotsArg
 
 template <int DK, int WARPS>
 cudaError_t launch_warps(const StepSlotsArgs &a, cudaStream_t stream) {
-  const size_t blocks = (size_t)a.R * a.H * (a.dv / rows_of(WARPS));
+  const size_t blocks = (size_t)a.R * a.H;
   if (blocks > 0x7fffffffu) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(WARPS * 32);
   if (a.bf16) {
@@ -455,7 +425,12 @@ cudaError_t launch_dk(const StepSlotsArgs &a, cudaStream_t stream) {
     }
     return cudaGetLastError();
   }
-  return a.dv == 32 ? launch_warps<DK, 4>(a, stream) : launch_warps<DK, 8>(a, stream);
+  switch (a.dv) {
+    case 32: return launch_warps<DK, 2>(a, stream);
+    case 64: return launch_warps<DK, 4>(a, stream);
+    case 128: return launch_warps<DK, 8>(a, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
