@@ -34,34 +34,39 @@ inline int norm_vector(const GroupNormArgs &a) {
   return 1;
 }
 
-// Weights or biases of one access, as pairs (`none` where there are none).
-template <int VEC>
-__device__ __forceinline__ void load_affine(const float *p, int at, bool in, float none, float2 *x) {
-  float v[VEC + VEC % 2];
+// A lane's weights or biases from p + at on (`none` where there are none).
+template <int VEC, int L, int NV>
+__device__ __forceinline__ void load_affine(const float *p, int at, const bool (&in)[NV], float none,
+                                            float2 (&x)[VEC * NV / 2]) {
+  float v[VEC * NV];
 #pragma unroll
-  for (int e = 0; e < VEC + VEC % 2; ++e) v[e] = none;
-  if (p && in) {
+  for (int i = 0; i < NV; ++i) {
+    float *w = v + i * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[e] = none;
+    if (!p || !in[i]) continue;
+    const float *from = p + at + i * L * VEC;
     if constexpr (VEC >= 4) {
 #pragma unroll
       for (int e = 0; e < VEC; e += 4) {
-        const float4 t = *reinterpret_cast<const float4 *>(p + at + e);
-        v[e] = t.x; v[e + 1] = t.y; v[e + 2] = t.z; v[e + 3] = t.w;
+        const float4 t = *reinterpret_cast<const float4 *>(from + e);
+        w[e] = t.x; w[e + 1] = t.y; w[e + 2] = t.z; w[e + 3] = t.w;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = p[at + e];
+      for (int e = 0; e < VEC; ++e) w[e] = from[e];
     }
   }
 #pragma unroll
-  for (int e = 0; e < VEC; e += 2) x[e / 2] = make_float2(v[e], v[e + 1]);
+  for (int e = 0; e < VEC * NV / 2; ++e) x[e] = make_float2(v[2 * e], v[2 * e + 1]);
 }
 
 // Subtracts the group's mean from x (with center; what lies outside the group
 // stays 0) and returns 1 / sqrt(mean square + eps).
 template <int VEC, int L, int NV>
-__device__ __forceinline__ float normalise(float2 (&x)[(VEC + 1) / 2 * NV], const bool (&in)[NV],
+__device__ __forceinline__ float normalise(float2 (&x)[VEC * NV / 2], const bool (&in)[NV],
                                            int center, float inv_d, float eps) {
-  constexpr int H = (VEC + 1) / 2, N = H * NV;
+  constexpr int N = VEC * NV / 2;
   if (center) {
     float2 sum = both(0.f);
 #pragma unroll
@@ -69,8 +74,8 @@ __device__ __forceinline__ float normalise(float2 (&x)[(VEC + 1) / 2 * NV], cons
     const float m = lanes_sum<L>(sum.x + sum.y) * inv_d;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      x[e].x = in[e / H] ? x[e].x - m : 0.f;
-      x[e].y = in[e / H] && VEC > 1 ? x[e].y - m : 0.f;
+      x[e].x = in[2 * e / VEC] ? x[e].x - m : 0.f;
+      x[e].y = in[(2 * e + 1) / VEC] ? x[e].y - m : 0.f;
     }
   }
   float2 ss = both(0.f);
@@ -80,7 +85,11 @@ __device__ __forceinline__ float normalise(float2 (&x)[(VEC + 1) / 2 * NV], cons
 }
 
 // Calls f.template operator()<T, VEC, L, NV>() for the layout of these
-// arguments: L lanes a group, NV accesses of VEC elements a lane.
+// arguments: L lanes a group, NV accesses of VEC elements a lane.  16-byte
+// accesses: one a lane where they fit, so that most rows are in flight.  Narrower
+// ones are bound by instructions, most of them the same for every group of a
+// warp: several accesses a lane and fewer lanes a group (33 channels of bf16, 1 M
+// groups: 32 lanes of 2 elements 194 us, 8 lanes of 8 elements 133 us).
 template <typename T, int VEC, typename F>
 cudaError_t norm_layout_vec(int D, F f) {
   const int n = (D + VEC - 1) / VEC;  // accesses of a group
@@ -88,15 +97,25 @@ cudaError_t norm_layout_vec(int D, F f) {
     if (n <= 4) return f.template operator()<T, VEC, 4, 1>();
     if (n <= 8) return f.template operator()<T, VEC, 8, 1>();
     if (n <= 16) return f.template operator()<T, VEC, 16, 1>();
-  }
-  if (n <= 32) return f.template operator()<T, VEC, 32, 1>();
-  if (n <= 64) return f.template operator()<T, VEC, 32, 2>();
-  if (n <= 128) return f.template operator()<T, VEC, 32, 4>();
-  if constexpr (VEC <= 4) {
+    if (n <= 32) return f.template operator()<T, VEC, 32, 1>();
+    if (n <= 64) return f.template operator()<T, VEC, 32, 2>();
+    if (n <= 128) return f.template operator()<T, VEC, 32, 4>();
+    if constexpr (VEC == 4) {
+      if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
+    }
+  } else if constexpr (VEC == 4) {
+    if (n <= 16) return f.template operator()<T, VEC, 8, 2>();
+    if (n <= 32) return f.template operator()<T, VEC, 16, 2>();
+    if (n <= 64) return f.template operator()<T, VEC, 32, 2>();
+    if (n <= 128) return f.template operator()<T, VEC, 32, 4>();
     if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
-  }
-  if constexpr (VEC == 1) {
+  } else {
+    if (n <= 32) return f.template operator()<T, VEC, 4, 8>();
+    if (n <= 64) return f.template operator()<T, VEC, 8, 8>();
+    if (n <= 128) return f.template operator()<T, VEC, 16, 8>();
+    if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
     if (n <= 512) return f.template operator()<T, VEC, 32, 16>();
+    if (n <= 640) return f.template operator()<T, VEC, 32, 20>();
     if (n <= 1024) return f.template operator()<T, VEC, 32, 32>();
   }
   return cudaErrorInvalidValue;

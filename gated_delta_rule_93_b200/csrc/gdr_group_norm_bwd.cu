@@ -54,7 +54,7 @@ template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_bwd_kernel(GroupNormArgs a, RowPlan p) {
   constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
-  constexpr int H = (VEC + 1) / 2, N = H * NV;  // pairs of an access and of a lane
+  constexpr int N = E / 2;  // pairs of a lane
   constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
   constexpr bool kAhead = !kQueue && E <= 16;  // (wider rows have no registers for a second one)
   constexpr int kPerBlock = kRowThreads / L;
@@ -64,12 +64,10 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   float2 w[N], b[N], dw[N], db[N];
   bool in[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * L + lane) * VEC;
-    in[i] = c < a.D;
-    load_affine<VEC>(a.weight, (a.per_channel ? g * a.D : 0) + c, in[i], 1.f, &w[i * H]);
-    load_affine<VEC>(a.bias, (a.per_channel ? g * a.D : 0) + c, in[i], 0.f, &b[i * H]);
-  }
+  for (int i = 0; i < NV; ++i) in[i] = (i * L + lane) * VEC < a.D;
+  const int channel = (a.per_channel ? g * a.D : 0) + lane * VEC;
+  load_affine<VEC, L, NV>(a.weight, channel, in, 1.f, w);
+  load_affine<VEC, L, NV>(a.bias, channel, in, 0.f, b);
 #pragma unroll
   for (int e = 0; e < N; ++e) dw[e] = db[e] = both(0.f);
   const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
@@ -139,14 +137,10 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
 #pragma unroll
     for (int u = 0; u < U; ++u, row += p.step) {
       float2 x[N], z[N], dy[N], h[N];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) unpack2<T, VEC>(xr[u][i], &x[i * H]);
+      unpack_row<T, VEC, NV>(xr[u], x);
       const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        unpack2<T, VEC>(zr[u][i], &z[i * H]);
-        unpack2<T, VEC>(dyr[u][i], &dy[i * H]);
-      }
+      unpack_row<T, VEC, NV>(zr[u], z);
+      unpack_row<T, VEC, NV>(dyr[u], dy);
       float hn;
       if (a.z) {
         if (a.act == GDR_ACT_SILU)
@@ -172,19 +166,16 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
         mean = lanes_sum<L>(sum.x + sum.y) * inv_d;
       }
 #pragma unroll
+      for (int e = 0; e < N; ++e)  // dx in place of h: rstd h - rstd mean - n (rstd hn)
+        h[e] = fma2(h[e], both(rstd), fma2(x[e], both(-rstd * hn), both(-rstd * mean)));
+#pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (row >= last || !in[i]) continue;
         const long long at = off + row * dense + i * L * VEC;
-        if (a.dz) store_vec2<T, VEC>(static_cast<T *>(a.dz) + at, &z[i * H]);
-        float2 d[H];
-#pragma unroll
-        for (int e = 0; e < H; ++e) {  // rstd h - rstd mean - n (rstd hn)
-          const float2 n = x[i * H + e];
-          d[e] = fma2(h[i * H + e], both(rstd), fma2(n, both(-rstd * hn), both(-rstd * mean)));
-        }
+        if (a.dz) store_access<T, VEC>(static_cast<T *>(a.dz) + at, z, i);
         constexpr int V4 = VEC < 4 ? VEC : 4;
 #pragma unroll
-        for (int e = 0; e < VEC; e += V4) store_vec2<float, V4>(a.dx + at + e, d + e / 2);
+        for (int e = 0; e < VEC; e += V4) store_access<float, V4>(a.dx + at + e, h, (i * VEC + e) / V4);
       }
     }
   }
@@ -203,8 +194,7 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float2 sums = (which ? db : dw)[e / VEC * H + e % VEC / 2];
-      float v = e % VEC % 2 ? sums.y : sums.x;
+      float v = element(which ? db : dw, e);
 #pragma unroll
       for (int m = L; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
       // (element e of a lane is channel ((e / VEC) L + lane) VEC + e % VEC)

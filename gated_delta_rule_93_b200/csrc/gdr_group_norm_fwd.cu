@@ -7,7 +7,7 @@ namespace {
 
 // Rows requested at a time (16 bytes of a tensor a lane), and blocks on an SM, for E elements a lane.
 constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
-constexpr int blocks_per_sm(int E) { return E <= 8 ? 4 : E <= 16 ? 2 : 1; }
+constexpr int blocks_per_sm(int E) { return E <= 8 ? 4 : E <= 20 ? 2 : 1; }
 
 constexpr int kTurns = 8;
 
@@ -30,22 +30,24 @@ template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_fwd_kernel(GroupNormArgs a, RowPlan p) {
   constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
-  constexpr int H = (VEC + 1) / 2, N = H * NV;  // pairs of an access and of a lane
+  constexpr int N = E / 2;  // pairs of a lane
   constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
   constexpr bool kAhead = !kQueue && E <= 16;  // (wider rows have no registers for a second one)
   const int lane = threadIdx.x % L;
   constexpr int kPerBlock = kRowThreads / L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
   const float inv_d = 1.f / (float)a.D;
+  constexpr bool kKeep = E <= 8;  // wider rows take their weights from L1 each time
   float2 w[N], b[N];
   bool in[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * L + lane) * VEC;
-    in[i] = c < a.D;
-    load_affine<VEC>(a.weight, (a.per_channel ? g * a.D : 0) + c, in[i], 1.f, &w[i * H]);
-    load_affine<VEC>(a.bias, (a.per_channel ? g * a.D : 0) + c, in[i], 0.f, &b[i * H]);
-  }
+  for (int i = 0; i < NV; ++i) in[i] = (i * L + lane) * VEC < a.D;
+  const auto affine = [&] {
+    const int c = (a.per_channel ? g * a.D : 0) + lane * VEC;
+    load_affine<VEC, L, NV>(a.weight, c, in, 1.f, w);
+    load_affine<VEC, L, NV>(a.bias, c, in, 0.f, b);
+  };
+  if constexpr (kKeep) affine();
   // (all lanes of a warp take every turn: the sums shuffle over whole warps)
   const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
   const T *xp = static_cast<const T *>(a.x) + (long long)g * a.D + lane * VEC;
@@ -109,12 +111,10 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
 #pragma unroll
     for (int u = 0; u < U; ++u, row += p.step) {
       float2 x[N], z[N];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        unpack2<T, VEC>(xr[u][i], &x[i * H]);
-        unpack2<T, VEC>(zr[u][i], &z[i * H]);
-      }
+      unpack_row<T, VEC, NV>(xr[u], x);
+      unpack_row<T, VEC, NV>(zr[u], z);
       const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
+      if constexpr (!kKeep) affine();
       if (a.z) {
         if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, true>(x, z, w, b, rstd);
         else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, true>(x, z, w, b, rstd);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (row < last && in[i])
-          store_vec2<T, VEC>(yp + row * a.G * a.D + i * L * VEC, &x[i * H]);
+          store_access<T, VEC>(yp + row * a.G * a.D + i * L * VEC, x, i);
     }
   }
 }

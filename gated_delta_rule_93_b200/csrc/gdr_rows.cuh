@@ -88,31 +88,27 @@ __device__ __forceinline__ void unpack(const Raw<T, VEC> &raw, float *x) {
   for (int e = 0; e < VEC; ++e) x[e] = to_f(u.t[e]);
 }
 
-// The same as pairs (a single element is the first of a pair with 0).
-template <typename T, int VEC>
-__device__ __forceinline__ void unpack2(const Raw<T, VEC> &raw, float2 *x) {
-  float v[VEC + VEC % 2] = {};
-  unpack<T, VEC>(raw, v);
+// NV accesses of a lane as pairs of elements, in order.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void unpack_row(const Raw<T, VEC> (&raw)[NV],
+                                           float2 (&x)[VEC * NV / 2]) {
+  static_assert(VEC * NV % 2 == 0);
+  float v[VEC * NV];
 #pragma unroll
-  for (int e = 0; e < VEC; e += 2) x[e / 2] = make_float2(v[e], v[e + 1]);
+  for (int i = 0; i < NV; ++i) unpack<T, VEC>(raw[i], v + i * VEC);
+#pragma unroll
+  for (int e = 0; e < VEC * NV / 2; ++e) x[e] = make_float2(v[2 * e], v[2 * e + 1]);
+}
+
+// Element j of a lane's pairs.
+template <int N>
+__device__ __forceinline__ float element(const float2 (&x)[N], int j) {
+  return j % 2 ? x[j / 2].y : x[j / 2].x;
 }
 
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T *p, float *x) {
   unpack<T, VEC>(load_raw<T, VEC>(p), x);
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T *p, const float *x);
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec2(T *p, const float2 *x) {
-  float v[VEC + VEC % 2];
-#pragma unroll
-  for (int e = 0; e < VEC; e += 2) {
-    v[e] = x[e / 2].x;
-    v[e + 1] = x[e / 2].y;
-  }
-  store_vec<T, VEC>(p, v);
 }
 
 template <typename T, int VEC>
@@ -124,6 +120,15 @@ __device__ __forceinline__ void store_vec(T *p, const float *x) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e) from_f(u.t[e], x[e]);
   *reinterpret_cast<Raw<T, VEC> *>(p) = u.b;
+}
+
+// Access i of a lane's pairs.
+template <typename T, int VEC, int N>
+__device__ __forceinline__ void store_access(T *p, const float2 (&x)[N], int i) {
+  float v[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = element(x, i * VEC + e);
+  store_vec<T, VEC>(p, v);
 }
 
 // A thread's own queue of 16-byte loads in shared memory, STAGES rows of TENSORS
