@@ -89,7 +89,7 @@ __device__ __forceinline__ float normalise(float2 (&x)[VEC * NV / 2], const bool
 // accesses: one a lane where they fit, so that most rows are in flight.  Narrower
 // ones are bound by instructions, most of them the same for every group of a
 // warp: several accesses a lane and fewer lanes a group (33 channels of bf16, 1 M
-// groups: 32 lanes of 2 elements 194 us, 8 lanes of 8 elements 133 us).
+// groups: 32 lanes of 2 elements 194 us, 8 lanes of 8 elements 89 us).
 template <typename T, int VEC, typename F>
 cudaError_t norm_layout_vec(int D, F f) {
   const int n = (D + VEC - 1) / VEC;  // accesses of a group

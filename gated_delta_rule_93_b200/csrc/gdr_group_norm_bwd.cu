@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
   constexpr int N = E / 2;  // pairs of a lane
   constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
-  constexpr bool kAhead = !kQueue && E <= 16;  // (wider rows have no registers for a second one)
+  // (single elements and wide rows have no registers for a second one)
+  constexpr bool kAhead = !kQueue && VEC > 1 && E <= 16;
   constexpr int kPerBlock = kRowThreads / L;
   const int lane = threadIdx.x % L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);

@@ -7,7 +7,9 @@ namespace {
 
 // Rows requested at a time (16 bytes of a tensor a lane), and blocks on an SM, for E elements a lane.
 constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
-constexpr int blocks_per_sm(int E) { return E <= 8 ? 4 : E <= 20 ? 2 : 1; }
+constexpr int blocks_per_sm(int E, int vec) {
+  return E <= 8 ? (vec == 1 ? 3 : 4) : E <= 20 ? 2 : 1;
+}
 
 constexpr int kTurns = 8;
 
@@ -27,12 +29,13 @@ __device__ __forceinline__ void finish(float2 (&x)[N], const float2 (&z)[N], con
 }
 
 template <typename T, int VEC, int L, int NV>
-__global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
+__global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV, VEC))
     group_norm_fwd_kernel(GroupNormArgs a, RowPlan p) {
   constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
   constexpr int N = E / 2;  // pairs of a lane
   constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
-  constexpr bool kAhead = !kQueue && E <= 16;  // (wider rows have no registers for a second one)
+  // (single elements and wide rows have no registers for a second one)
+  constexpr bool kAhead = !kQueue && VEC > 1 && E <= 16;
   const int lane = threadIdx.x % L;
   constexpr int kPerBlock = kRowThreads / L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
@@ -138,7 +141,7 @@ struct Launch {
   template <typename T, int VEC, int L, int NV>
   cudaError_t operator()() const {
     const RowPlan p =
-        row_plan(a.rows, a.G, kRowThreads / L, kTurns, kSMs * blocks_per_sm(VEC * NV), false);
+        row_plan(a.rows, a.G, kRowThreads / L, kTurns, kSMs * blocks_per_sm(VEC * NV, VEC), false);
     group_norm_fwd_kernel<T, VEC, L, NV><<<p.blocks, kRowThreads, 0, stream>>>(a, p);
     return cudaGetLastError();
   }

@@ -118,9 +118,13 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
   constexpr int SH = NV == 8 ? 0 : NV == 4 ? 1 : 2;
   __shared__ Prepared<DK, WARPS, PERCH> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int blocks_per_head = a.dv / kRows;
+  const unsigned rh = blockIdx.x / blocks_per_head;
+  const int r = rh / a.H, h = rh % a.H;
   const int hk = h / (a.H / a.Hk);
-  const int row0 = warp * kWarpRows + (lane >> 3);  // this thread's rows: row0 + 4 i
+  const int block_row = blockIdx.x % blocks_per_head * kRows;
+  const int in_block = warp * kWarpRows + (lane >> 3);  // this thread's rows: in_block + 4 i
+  const int row0 = block_row + in_block;
   const int col0 = (lane & 7) * 4;
 
   int t0 = r, t1 = r + 1;
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
 #pragma unroll
       for (int e = 0; e < kRows / 32; ++e)
         sm.v[j][lane + 32 * e] =
-            load_in(a.v, t * a.v_stride + (size_t)h * a.dv + lane + 32 * e, BF16);
+            load_in(a.v, t * a.v_stride + (size_t)h * a.dv + block_row + lane + 32 * e, BF16);
       const float scale = a.gate_scale ? a.gate_scale[h] : 0.f;
       float kk = 0.f, qq = 0.f, kq = 0.f, rk = 1.f, rq = 1.f;
 #pragma unroll
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
       const size_t to = ((size_t)(tb + j) * a.H + h) * a.dv;
       const int idx = (lane & 7) >> SH;   // the dot product this lane ends up with
       const int mine = idx % RPT;         // its row: p for idx < RPT, r after
-      const float v = sm.v[j][row0 + 4 * mine];
+      const float v = sm.v[j][in_block + 4 * mine];
       float2 p2[RPT] = {}, r2[RPT] = {}, kr[2 * NC];
       float2 al = both(0.f);
       if constexpr (!PERCH) al = both(sm.al[j][0]);
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(128, 7) gdr_step_slots_one_kernel(StepSlotsArg
 
 template <int DK, int WARPS>
 cudaError_t launch_warps(const StepSlotsArgs &a, cudaStream_t stream) {
-  const size_t blocks = (size_t)a.R * a.H;
+  const size_t blocks = (size_t)a.R * a.H * (a.dv / rows_of(WARPS));
   if (blocks > 0x7fffffffu) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(WARPS * 32);
   if (a.bf16) {
@@ -425,12 +429,8 @@ cudaError_t launch_dk(const StepSlotsArgs &a, cudaStream_t stream) {
     }
     return cudaGetLastError();
   }
-  switch (a.dv) {
-    case 32: return launch_warps<DK, 2>(a, stream);
-    case 64: return launch_warps<DK, 4>(a, stream);
-    case 128: return launch_warps<DK, 8>(a, stream);
-  }
-  return cudaErrorInvalidValue;
+  constexpr int kWarps = 4;
+  return a.dv == 32 ? launch_warps<DK, 2>(a, stream) : launch_warps<DK, kWarps>(a, stream);
 }
 
 }  // namespace

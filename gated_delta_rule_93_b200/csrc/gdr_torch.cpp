@@ -13,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -195,7 +196,8 @@ class Call {
   }
 
   at::Tensor make(at::IntArrayRef size, at::ScalarType type) {
-    at::Tensor t = at::empty(size, at::TensorOptions().dtype(type).device(guard_.current_device()));
+    // (as at::empty, without its way through the dispatcher: 1 us of 2)
+    at::Tensor t = at::detail::empty_cuda(size, type, guard_.current_device(), std::nullopt);
     if (other_ && t.numel()) t.record_stream(stream_.unwrap());
     return t;
   }
