@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   // Partial rows of the weight gradients, a block's D values each, db behind dw:
   // over the slots of a warp, then over the warps.
   if (!a.dweight && !a.dbias) return;
+  let_next();
   __shared__ float s[kRowThreads / 32][L * E];
   const int warp = threadIdx.x / 32, at = threadIdx.x % 32;
 #pragma unroll
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
 // Columns of dweight, then (second half of the grid's y) of dbias.
 __global__ void __launch_bounds__(1024) group_norm_sum_kernel(const float *part, int rows, int cols,
                                                               float *dweight, float *dbias) {
+  after_previous();
   float *out = blockIdx.y ? dbias : dweight;
   if (out)
     sum_columns(part + (blockIdx.y ? (size_t)rows * cols : 0), rows, cols, out, blockIdx.x);
@@ -245,7 +247,8 @@ struct Launch {
       const int rows = a.per_channel ? p.blocks / a.G : p.blocks;
       const int cols = a.per_channel ? a.G * a.D : a.D;
       const dim3 grid((cols + sum_width(cols) - 1) / sum_width(cols), a.dbias ? 2 : 1);
-      group_norm_sum_kernel<<<grid, 1024, 0, stream>>>(a.ws, rows, cols, a.dweight, a.dbias);
+      return launch_next(group_norm_sum_kernel, grid, 1024, stream, a.ws, rows, cols, a.dweight,
+                         a.dbias);
     }
     return cudaGetLastError();
   }

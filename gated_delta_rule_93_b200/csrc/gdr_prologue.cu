@@ -22,7 +22,7 @@ namespace {
 
 constexpr float kNormEps = 1e-6f;
 constexpr int kNormTurns = 4, kNormBlocks = 4 * kSMs;
-constexpr int kGateBlocks = 8 * kSMs;  // at most
+constexpr int kGateTurns = 4, kGateBlocks = 4 * kSMs;
 
 // The gates' blocks: `heads` heads of `tokens` tokens at a time; blocks that
 // share a tile of heads are `step` tokens apart.
@@ -44,9 +44,13 @@ GatePlan gate_plan(long long tokens, int H, int dk, int per_channel) {
   p.heads = per_channel ? 1 : H < slots ? H : slots;
   p.tiles = (H + p.heads - 1) / p.heads;
   p.tokens = slots / p.heads;
-  long long rows = (tokens + p.tokens - 1) / p.tokens;
-  if (rows > kGateBlocks / p.tiles) rows = kGateBlocks / p.tiles;
+  // a slot takes kGateTurns tokens, or fewer where that leaves less than kGateBlocks blocks
+  const long long passes = (tokens + p.tokens - 1) / p.tokens;
+  long long rows = (passes + kGateTurns - 1) / kGateTurns;
+  const int least = (kGateBlocks + p.tiles - 1) / p.tiles;
+  if (rows < least) rows = passes < least ? passes : least;
   if (rows < 1) rows = 1;
+  if (rows > (1 << 24) / p.tiles) rows = (1 << 24) / p.tiles;
   p.blocks = (int)(rows * p.tiles);
   p.step = rows * p.tokens;
   return p;
@@ -70,21 +74,35 @@ __device__ __forceinline__ GatePlace gate_place(const PrologueArgs &a, const Gat
 
 // g and beta of one block's gates.
 __device__ __forceinline__ void gates_fwd(const PrologueArgs &a, const GatePlan &p, int block) {
+  constexpr int U = 4;  // tokens on their way at once
   const GatePlace g = gate_place(a, p, block);
   if (!g.used) return;
   const float s = -a.gate_scale[g.h];
-#pragma unroll 2
-  for (long long t = g.token; t < a.tokens; t += p.step) {
-    const long long th = t * a.H + g.h;
-    if (g.lane == 0) a.beta[th] = sigmoid(__ldcs(a.b + th));
-    if (!a.per_channel) {
-      a.g[th] = s * softplus(__ldcs(a.a + th));
-    } else {
-      float x[4];
-      load_vec<float, 4>(a.a + th * a.d + 4 * g.lane, x);
+  for (long long t = g.token; t < a.tokens; t += U * p.step) {
+    float b[U], x[U][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = s * softplus(x[e]);
-      store_vec<float, 4>(a.g + th * a.d + 4 * g.lane, x);
+    for (int u = 0; u < U; ++u) {
+      const long long at = t + u * p.step, th = at * a.H + g.h;
+      if (at >= a.tokens) continue;
+      if (g.lane == 0) b[u] = __ldcs(a.b + th);
+      if (!a.per_channel)
+        x[u][0] = __ldcs(a.a + th);
+      else
+        load_vec<float, 4>(a.a + th * a.d + 4 * g.lane, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long at = t + u * p.step, th = at * a.H + g.h;
+      if (at >= a.tokens) continue;
+      if (g.lane == 0) a.beta[th] = sigmoid(b[u]);
+      if (!a.per_channel) {
+        a.g[th] = s * softplus(x[u][0]);
+      } else {
+        const float2 lo = mul2(both(s), softplus2(make_float2(x[u][0], x[u][1])));
+        const float2 hi = mul2(both(s), softplus2(make_float2(x[u][2], x[u][3])));
+        const float y[4] = {lo.x, lo.y, hi.x, hi.y};
+        store_vec<float, 4>(a.g + th * a.d + 4 * g.lane, y);
+      }
     }
   }
 }
@@ -122,17 +140,22 @@ __device__ __forceinline__ void gates_bwd(const PrologueArgs &a, const GatePlan 
           const float beta = sigmoid(b[u]);
           a.db[th] = beta * (1.f - beta) * dbeta[u];
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (e && !a.per_channel) break;
+        if (!a.per_channel) {
           float sig;
-          ds -= dg[u][e] * softplus(x[u][e], &sig);
-          x[u][e] = -s * sig * dg[u][e];
+          ds -= dg[u][0] * softplus(x[u][0], &sig);
+          a.da[th] = -s * sig * dg[u][0];
+        } else {
+          float2 sum = both(0.f), y[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 d = make_float2(dg[u][2 * e], dg[u][2 * e + 1]);
+            float2 sig;
+            sum = fma2(d, softplus2(make_float2(x[u][2 * e], x[u][2 * e + 1]), &sig), sum);
+            y[e] = mul2(mul2(both(-s), sig), d);
+          }
+          ds -= sum.x + sum.y;
+          store_access<float, 4>(a.da + th * a.d + 4 * g.lane, y, 0);
         }
-        if (!a.per_channel)
-          a.da[th] = x[u][0];
-        else
-          store_vec<float, 4>(a.da + th * a.d + 4 * g.lane, x[u]);
       }
     }
   }
@@ -263,6 +286,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) prologue_bwd_kernel(PrologueAr
 
 __global__ void __launch_bounds__(1024) prologue_sum_kernel(const float *part, int rows, int cols,
                                                             float *out) {
+  after_previous();
   sum_columns(part, rows, cols, out, blockIdx.x);
 }
 
@@ -278,8 +302,8 @@ cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
     if (p.gate.blocks > p.gate.tiles) {
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      prologue_sum_kernel<<<(a.H + sum_width(a.H) - 1) / sum_width(a.H), 1024, 0, stream>>>(
-          a.ws, p.gate.blocks / p.gate.tiles, a.H, a.dgate_scale);
+      return launch_next(prologue_sum_kernel, dim3((a.H + sum_width(a.H) - 1) / sum_width(a.H)), 1024,
+                         stream, a.ws, p.gate.blocks / p.gate.tiles, a.H, a.dgate_scale);
     }
   }
   return cudaGetLastError();

@@ -201,11 +201,59 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   return e;
 }
 
-// log(1 + e^x), with no branch that overflows, and 1 / (1 + e^-x) from the same exponential.
+// log(1 + e^x) = max(x, 0) + log(1 + e) with e = e^-|x| <= 1, and 1 / (1 + e^-x) from the same e.
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by its series up to s^13 (the rest is
+// below 2e-8 of it): relative error about 4 2^-23 for every x, in place of log1pf's longer
+// way (a per-channel prologue of 8192 x 16 x 128: 64 us with log1pf, 50 us).
+__device__ __forceinline__ float2 softplus2(float2 x, float2 *sig = nullptr) {
+  float2 e = mul2(make_float2(fabsf(x.x), fabsf(x.y)), both(-1.4426950408889634f)), r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+  const float2 d = add2(e, both(2.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  const float2 s = mul2(e, r), t = mul2(s, s);
+  float2 p = fma2(t, both(1.f / 13), both(1.f / 11));
+  p = fma2(t, p, both(1.f / 9));
+  p = fma2(t, p, both(1.f / 7));
+  p = fma2(t, p, both(1.f / 5));
+  p = fma2(t, p, both(1.f / 3));
+  p = fma2(t, p, both(1.f));
+  if (sig) {
+    const float2 o = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(o.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(o.y));
+    *sig = mul2(r, make_float2(x.x >= 0.f ? 1.f : e.x, x.y >= 0.f ? 1.f : e.y));
+  }
+  return fma2(add2(s, s), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
 __device__ __forceinline__ float softplus(float x, float *sig = nullptr) {
-  const float e = __expf(-fabsf(x));
-  if (sig) *sig = __fdividef(x >= 0.f ? 1.f : e, 1.f + e);
-  return fmaxf(x, 0.f) + log1pf(e);
+  float2 both_sig;
+  const float2 y = softplus2(both(x), sig ? &both_sig : nullptr);
+  if (sig) *sig = both_sig.x;
+  return y.x;
+}
+
+// Launches `kernel` so that it may be set up while the one before it ends; it has to
+// begin with after_previous().
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, P(args)...);
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // out[c] = sum over k of part[k * cols + c], in a fixed order.  A block of 1024
