@@ -22,7 +22,7 @@ namespace {
 
 constexpr float kNormEps = 1e-6f;
 constexpr int kNormTurns = 4, kNormBlocks = 4 * kSMs;
-constexpr int kGateTurns = 4, kGateBlocks = 4 * kSMs;
+constexpr int kGateTurns = 8, kGateBlocks = 4 * kSMs;
 
 // The gates' blocks: `heads` heads of `tokens` tokens at a time; blocks that
 // share a tile of heads are `step` tokens apart.
@@ -226,12 +226,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) prologue_fwd_kernel(PrologueAr
 }
 
 template <typename T, int VEC, int L>
-__global__ void __launch_bounds__(kRowThreads, 3) prologue_bwd_kernel(PrologueArgs a, Split p) {
-  if ((int)blockIdx.x < p.gate.blocks) {
-    gates_bwd(a, p.gate, blockIdx.x);
+__global__ void __launch_bounds__(kRowThreads, 4) prologue_bwd_kernel(PrologueArgs a, Split p) {
+  const int block = blockIdx.x;
+  if (block >= p.norm.blocks) {
+    gates_bwd(a, p.gate, block - p.norm.blocks);
     return;
   }
-  const int block = blockIdx.x - p.gate.blocks;
   const int lane = threadIdx.x % L;
   constexpr int kPerBlock = kRowThreads / L;
   const int slot = threadIdx.x / L, hk = p.norm.group(block, slot, kPerBlock, a.Hk);
@@ -242,44 +242,38 @@ __global__ void __launch_bounds__(kRowThreads, 3) prologue_bwd_kernel(PrologueAr
   const long long turns = (a.tokens + p.norm.step - 1) / p.norm.step;
   long long t = p.norm.first_row(block, slot, kPerBlock, a.Hk);
   for (long long k = 0; k < turns; ++k, t += p.norm.step) {
-    float d[2][VEC] = {};
-    Raw<T, VEC> raw[2] = {};
-    if (t < last) {
-      raw[0] = load_raw<T, VEC>(static_cast<const T *>(a.q) + t * a.q_stride + in);
-      raw[1] = load_raw<T, VEC>(static_cast<const T *>(a.k) + t * a.k_stride + in);
-#pragma unroll 2
-      for (int s = 0; s < share; ++s) {
-        const long long at = (t * a.H + s) * a.d + up;
-        float u[2][VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; e += 4) {
-          load_vec<float, 4>(a.dqn + at + e, &u[0][e]);
-          load_vec<float, 4>(a.dkn + at + e, &u[1][e]);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          d[0][e] += u[0][e];
-          d[1][e] += u[1][e];
-        }
-      }
-    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
+      float d[VEC] = {};
+      Raw<T, VEC> raw = {};
+      if (t < last) {
+        raw = load_raw<T, VEC>(static_cast<const T *>(which ? a.k : a.q) +
+                               t * (which ? a.k_stride : a.q_stride) + in);
+        const float *from = (which ? a.dkn : a.dqn) + t * a.H * a.d + up;
+#pragma unroll 2
+        for (int s = 0; s < share; ++s) {
+          float u[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; e += 4) load_vec<float, 4>(from + s * a.d + e, u + e);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) d[e] += u[e];
+        }
+      }
       if (a.norm_qk & (which ? GDR_NORM_K : GDR_NORM_Q)) {
         float x[VEC], ss = 0.f, dot = 0.f;
-        unpack<T, VEC>(raw[which], x);
+        unpack<T, VEC>(raw, x);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           ss += x[e] * x[e];
-          dot += x[e] * d[which][e];
+          dot += x[e] * d[e];
         }
         const float r = rsqrtf(lanes_sum<L>(ss) + kNormEps);
         dot = lanes_sum<L>(dot) * r;  // q^ . G
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) d[which][e] = r * (d[which][e] - x[e] * r * dot);
+        for (int e = 0; e < VEC; ++e) d[e] = r * (d[e] - x[e] * r * dot);
       }
       if (t < last)
-        store_vec<T, VEC>(static_cast<T *>(which ? a.dk : a.dq) + t * a.Hk * a.d + in, d[which]);
+        store_vec<T, VEC>(static_cast<T *>(which ? a.dk : a.dq) + t * a.Hk * a.d + in, d);
     }
   }
 }
