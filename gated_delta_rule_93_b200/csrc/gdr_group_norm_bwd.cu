@@ -11,8 +11,7 @@
 namespace gdr {
 namespace {
 
-// Rows requested at a time (16 bytes of a tensor a lane), and blocks on an SM, for E elements a lane.
-constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
+// Blocks on an SM for E elements a lane.
 constexpr int blocks_per_sm(int E) { return E <= 8 ? 2 : 1; }
 
 // N pairs of a row.  On return x holds n and z dz; h, the running dw and db are
@@ -53,11 +52,7 @@ __device__ __forceinline__ float gradients(float2 (&x)[N], float2 (&z)[N], const
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_bwd_kernel(GroupNormArgs a, RowPlan p) {
-  constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
-  constexpr int N = E / 2;  // pairs of a lane
-  constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
-  // (single elements and wide rows have no registers for a second one)
-  constexpr bool kAhead = !kQueue && VEC > 1 && E <= 16;
+  constexpr int E = VEC * NV, N = E / 2;  // elements and pairs of a lane
   constexpr int kPerBlock = kRowThreads / L;
   const int lane = threadIdx.x % L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
@@ -71,113 +66,113 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   load_affine<VEC, L, NV>(a.bias, channel, in, 0.f, b);
 #pragma unroll
   for (int e = 0; e < N; ++e) dw[e] = db[e] = both(0.f);
-  const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
+  const long long first = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
+  const int mine = p.count(p.used(blockIdx.x, slot, kPerBlock), first, a.rows);
   const long long off = (long long)g * a.D + lane * VEC, dense = (long long)a.G * a.D;
-  const T *xp = static_cast<const T *>(a.x) + off, *zp = static_cast<const T *>(a.z) + off;
-  const T *dyp = static_cast<const T *>(a.dy) + off;
-  const long long turns = (a.rows + U * p.step - 1) / (U * p.step);
-  long long row = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
-  // 16-byte accesses wait in shared memory, 3 rows of them; others a turn ahead in registers.
-  constexpr int kStages = 3;
-  __shared__ uint4 waiting[kQueue ? kStages : 1][3][kRowThreads];
-  Queue<3, kStages> queue{waiting};
-  const auto ask = [&](long long at, int stage) {
-    if (at < last && in[0]) {
-      queue.request(stage, 0, xp + at * a.x_stride);
-      if (a.z) queue.request(stage, 1, zp + at * a.z_stride);
-      queue.request(stage, 2, dyp + at * dense);
+  const T *xp = static_cast<const T *>(a.x) + off + first * a.x_stride;  // the row asked for next
+  const T *zp = static_cast<const T *>(a.z) + off + first * a.z_stride;
+  const T *dyp = static_cast<const T *>(a.dy) + off + first * dense;
+  long long out = off + first * dense;  // of dx and dz
+  const long long x_step = p.step * a.x_stride, z_step = p.step * a.z_stride;
+  const long long step = p.step * dense;
+
+  // The queue's memory takes the sums over the block at the end.
+  constexpr bool kQueue = norm_queue<T, VEC, NV>;
+  constexpr int kStages = NV == 1 ? 3 : 2;
+  constexpr int kWaiting = kQueue ? 3 * NV : 1;
+  using Waiting = Raw<T, VEC>[kQueue ? kStages : 1][kWaiting][kRowThreads];
+  using Sums = float[kRowThreads / 32][L * E];
+  __shared__ __align__(16) unsigned char memory[sizeof(Waiting) > sizeof(Sums) ? sizeof(Waiting)
+                                                                              : sizeof(Sums)];
+  Queue<Raw<T, VEC>, kWaiting, kStages> queue{*reinterpret_cast<Waiting *>(memory)};
+  const auto ask = [&](int turn, int stage) {
+    if (turn < mine) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (in[i]) {
+          queue.request(stage, i, xp + i * L * VEC);
+          queue.request(stage, NV + i, dyp + i * L * VEC);
+          if (a.z) queue.request(stage, 2 * NV + i, zp + i * L * VEC);
+        }
     }
     queue.commit();
+    xp += x_step;
+    zp += z_step;
+    dyp += step;
   };
-  Raw<T, VEC> xn[U][NV], zn[U][NV], dyn[U][NV];  // the next turn's rows
-  const auto request = [&](long long from) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const long long at = from + u * p.step;
-        xn[u][i] = zn[u][i] = dyn[u][i] = Raw<T, VEC>{};
-        if (at < last && in[i]) {
-          xn[u][i] = load_raw<T, VEC>(xp + at * a.x_stride + i * L * VEC);
-          dyn[u][i] = load_raw<T, VEC>(dyp + at * dense + i * L * VEC);
-          if (a.z) zn[u][i] = load_raw<T, VEC>(zp + at * a.z_stride + i * L * VEC);
-        }
-      }
-  };
-  if constexpr (kAhead) request(row);
   if constexpr (kQueue) {
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) ask(row + i * p.step, i);
+    for (int i = 0; i < kStages - 1; ++i) ask(i, i);
   }
   int stage = 0;
-  for (long long k = 0; k < turns; ++k) {
-    Raw<T, VEC> xr[U][NV], zr[U][NV], dyr[U][NV];
+  for (int k = 0; k < p.turns; ++k, out += step) {
+    const bool live = k < mine;
+    Raw<T, VEC> xr[NV], zr[NV], dyr[NV];
     if constexpr (kQueue) {
-      ask(row + (kStages - 1) * p.step, stage == 0 ? kStages - 1 : stage - 1);
+      ask(k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
       queue.wait();
-      const bool live = row < last && in[0];
-      const uint4 x16 = live ? queue.get(stage, 0) : uint4{};
-      const uint4 z16 = live && a.z ? queue.get(stage, 1) : uint4{};
-      const uint4 dy16 = live ? queue.get(stage, 2) : uint4{};
-      xr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&x16);
-      zr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&z16);
-      dyr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&dy16);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-    } else {
-      if constexpr (!kAhead) request(row);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          xr[u][i] = xn[u][i];
-          zr[u][i] = zn[u][i];
-          dyr[u][i] = dyn[u][i];
-        }
-      if constexpr (kAhead) request(row + U * p.step);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u, row += p.step) {
-      float2 x[N], z[N], dy[N], h[N];
-      unpack_row<T, VEC, NV>(xr[u], x);
-      const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
-      unpack_row<T, VEC, NV>(zr[u], z);
-      unpack_row<T, VEC, NV>(dyr[u], dy);
-      float hn;
-      if (a.z) {
-        if (a.act == GDR_ACT_SILU)
-          hn = gradients<GDR_ACT_SILU, true>(x, z, dy, w, b, rstd, h, dw, db);
-        else if (a.act == GDR_ACT_SIGMOID)
-          hn = gradients<GDR_ACT_SIGMOID, true>(x, z, dy, w, b, rstd, h, dw, db);
-        else
-          hn = gradients<GDR_ACT_NONE, true>(x, z, dy, w, b, rstd, h, dw, db);
+    for (int i = 0; i < NV; ++i) {
+      xr[i] = zr[i] = dyr[i] = Raw<T, VEC>{};
+      if (!live || !in[i]) continue;
+      if constexpr (kQueue) {
+        xr[i] = queue.get(stage, i);
+        dyr[i] = queue.get(stage, NV + i);
+        if (a.z) zr[i] = queue.get(stage, 2 * NV + i);
       } else {
-        if (a.act == GDR_ACT_SILU)
-          hn = gradients<GDR_ACT_SILU, false>(x, z, dy, w, b, rstd, h, dw, db);
-        else if (a.act == GDR_ACT_SIGMOID)
-          hn = gradients<GDR_ACT_SIGMOID, false>(x, z, dy, w, b, rstd, h, dw, db);
-        else
-          hn = gradients<GDR_ACT_NONE, false>(x, z, dy, w, b, rstd, h, dw, db);
+        xr[i] = load_raw<T, VEC>(xp + i * L * VEC);
+        dyr[i] = load_raw<T, VEC>(dyp + i * L * VEC);
+        if (a.z) zr[i] = load_raw<T, VEC>(zp + i * L * VEC);
       }
-      hn = lanes_sum<L>(hn) * inv_d;
-      float mean = 0.f;  // of h
-      if (a.center) {
-        float2 sum = both(0.f);
+    }
+    if constexpr (kQueue) {
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      xp += x_step;
+      zp += z_step;
+      dyp += step;
+    }
+    float2 x[N], z[N], dy[N], h[N];
+    unpack_row<T, VEC, NV>(xr, x);
+    const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
+    unpack_row<T, VEC, NV>(zr, z);
+    unpack_row<T, VEC, NV>(dyr, dy);
+    float hn;
+    if (a.z) {
+      if (a.act == GDR_ACT_SILU)
+        hn = gradients<GDR_ACT_SILU, true>(x, z, dy, w, b, rstd, h, dw, db);
+      else if (a.act == GDR_ACT_SIGMOID)
+        hn = gradients<GDR_ACT_SIGMOID, true>(x, z, dy, w, b, rstd, h, dw, db);
+      else
+        hn = gradients<GDR_ACT_NONE, true>(x, z, dy, w, b, rstd, h, dw, db);
+    } else {
+      if (a.act == GDR_ACT_SILU)
+        hn = gradients<GDR_ACT_SILU, false>(x, z, dy, w, b, rstd, h, dw, db);
+      else if (a.act == GDR_ACT_SIGMOID)
+        hn = gradients<GDR_ACT_SIGMOID, false>(x, z, dy, w, b, rstd, h, dw, db);
+      else
+        hn = gradients<GDR_ACT_NONE, false>(x, z, dy, w, b, rstd, h, dw, db);
+    }
+    hn = lanes_sum<L>(hn) * inv_d;
+    float mean = 0.f;  // of h
+    if (a.center) {
+      float2 sum = both(0.f);
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum = add2(sum, h[e]);
-        mean = lanes_sum<L>(sum.x + sum.y) * inv_d;
-      }
+      for (int e = 0; e < N; ++e) sum = add2(sum, h[e]);
+      mean = lanes_sum<L>(sum.x + sum.y) * inv_d;
+    }
 #pragma unroll
-      for (int e = 0; e < N; ++e)  // dx in place of h: rstd h - rstd mean - n (rstd hn)
-        h[e] = fma2(h[e], both(rstd), fma2(x[e], both(-rstd * hn), both(-rstd * mean)));
+    for (int e = 0; e < N; ++e)  // dx in place of h: rstd h - rstd mean - n (rstd hn)
+      h[e] = fma2(h[e], both(rstd), fma2(x[e], both(-rstd * hn), both(-rstd * mean)));
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (row >= last || !in[i]) continue;
-        const long long at = off + row * dense + i * L * VEC;
-        if (a.dz) store_access<T, VEC>(static_cast<T *>(a.dz) + at, z, i);
-        constexpr int V4 = VEC < 4 ? VEC : 4;
+    for (int i = 0; i < NV; ++i) {
+      if (!live || !in[i]) continue;
+      const long long at = out + i * L * VEC;
+      if (a.dz) store_access<T, VEC>(static_cast<T *>(a.dz) + at, z, i);
+      constexpr int V4 = VEC < 4 ? VEC : 4;
 #pragma unroll
-        for (int e = 0; e < VEC; e += V4) store_access<float, V4>(a.dx + at + e, h, (i * VEC + e) / V4);
-      }
+      for (int e = 0; e < VEC; e += V4) store_access<float, V4>(a.dx + at + e, h, (i * VEC + e) / V4);
     }
   }
 
@@ -185,14 +180,14 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   // over the slots of a warp, then over the warps.
   if (!a.dweight && !a.dbias) return;
   let_next();
-  __shared__ float s[kRowThreads / 32][L * E];
+  Sums &s = *reinterpret_cast<Sums *>(memory);  // (no request is left)
   const int warp = threadIdx.x / 32, at = threadIdx.x % 32;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float *out = which ? a.dbias : a.dweight;
-    if (!out) continue;
-    if (p.sum) out = a.ws + ((which ? (long long)p.blocks : 0) + blockIdx.x) * a.D;
-    else if (p.by_block) out += (long long)g * a.D;
+    float *to = which ? a.dbias : a.dweight;
+    if (!to) continue;
+    if (p.sum) to = a.ws + ((which ? (long long)p.blocks : 0) + blockIdx.x) * a.D;
+    else if (p.by_block) to += (long long)g * a.D;
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -207,7 +202,7 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < kRowThreads / 32; ++i) v += s[i][c];
-      out[c] = v;
+      to[c] = v;
     }
   }
 }

@@ -5,13 +5,11 @@
 namespace gdr {
 namespace {
 
-// Rows requested at a time (16 bytes of a tensor a lane), and blocks on an SM, for E elements a lane.
-constexpr int rows_ahead(int bytes) { return bytes <= 4 ? 4 : bytes <= 8 ? 2 : 1; }
+// Blocks on an SM for E elements a lane in accesses of `vec`.
 constexpr int blocks_per_sm(int E, int vec) {
   return E <= 8 ? (vec == 1 ? 3 : 4) : E <= 20 ? 2 : 1;
 }
-
-constexpr int kTurns = 8;
+constexpr int kTurns = 8;  // rows of a lane in a block
 
 // y of N pairs in place of x: x are normalised but for rstd.
 template <int ACT, bool GATED, int N>
@@ -31,13 +29,9 @@ __device__ __forceinline__ void finish(float2 (&x)[N], const float2 (&z)[N], con
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV, VEC))
     group_norm_fwd_kernel(GroupNormArgs a, RowPlan p) {
-  constexpr int E = VEC * NV, U = rows_ahead(E * sizeof(T));
-  constexpr int N = E / 2;  // pairs of a lane
-  constexpr bool kQueue = sizeof(Raw<T, VEC>) == 16 && NV == 1;
-  // (single elements and wide rows have no registers for a second one)
-  constexpr bool kAhead = !kQueue && VEC > 1 && E <= 16;
-  const int lane = threadIdx.x % L;
+  constexpr int E = VEC * NV, N = E / 2;  // elements and pairs of a lane
   constexpr int kPerBlock = kRowThreads / L;
+  const int lane = threadIdx.x % L;
   const int slot = threadIdx.x / L, g = p.group(blockIdx.x, slot, kPerBlock, a.G);
   const float inv_d = 1.f / (float)a.D;
   constexpr bool kKeep = E <= 8;  // wider rows take their weights from L1 each time
@@ -52,86 +46,79 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV, VEC))
   };
   if constexpr (kKeep) affine();
   // (all lanes of a warp take every turn: the sums shuffle over whole warps)
-  const long long last = p.used(blockIdx.x, slot, kPerBlock) ? a.rows : 0;  // rows of this slot end here
-  const T *xp = static_cast<const T *>(a.x) + (long long)g * a.D + lane * VEC;
-  const T *zp = static_cast<const T *>(a.z) + (long long)g * a.D + lane * VEC;
-  T *yp = static_cast<T *>(a.y) + (long long)g * a.D + lane * VEC;
-  const long long turns = (a.rows + U * p.step - 1) / (U * p.step);
-  long long row = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
-  // 16-byte accesses wait in shared memory, 4 rows of them; others a turn ahead in registers.
-  constexpr int kStages = 4;
-  __shared__ uint4 waiting[kQueue ? kStages : 1][2][kRowThreads];
-  Queue<2, kStages> queue{waiting};
-  const auto ask = [&](long long at, int stage) {
-    if (at < last && in[0]) {
-      queue.request(stage, 0, xp + at * a.x_stride);
-      if (a.z) queue.request(stage, 1, zp + at * a.z_stride);
-    }
-    queue.commit();
-  };
-  Raw<T, VEC> xn[U][NV], zn[U][NV];  // the next turn's rows
-  const auto request = [&](long long from) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const long long at = from + u * p.step;
-        xn[u][i] = zn[u][i] = Raw<T, VEC>{};
-        if (at < last && in[i]) {
-          xn[u][i] = load_raw<T, VEC>(xp + at * a.x_stride + i * L * VEC);
-          if (a.z) zn[u][i] = load_raw<T, VEC>(zp + at * a.z_stride + i * L * VEC);
-        }
-      }
-  };
-  if constexpr (kAhead) request(row);
-  if constexpr (kQueue) {
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) ask(row + i * p.step, i);
-  }
-  int stage = 0;
-  for (long long k = 0; k < turns; ++k) {
-    Raw<T, VEC> xr[U][NV], zr[U][NV];
-    if constexpr (kQueue) {
-      ask(row + (kStages - 1) * p.step, stage == 0 ? kStages - 1 : stage - 1);
-      queue.wait();
-      const bool live = row < last && in[0];
-      const uint4 x16 = live ? queue.get(stage, 0) : uint4{};
-      const uint4 z16 = live && a.z ? queue.get(stage, 1) : uint4{};
-      xr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&x16);
-      zr[0][0] = *reinterpret_cast<const Raw<T, VEC> *>(&z16);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-    } else {
-      if constexpr (!kAhead) request(row);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          xr[u][i] = xn[u][i];
-          zr[u][i] = zn[u][i];
-        }
-      if constexpr (kAhead) request(row + U * p.step);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u, row += p.step) {
-      float2 x[N], z[N];
-      unpack_row<T, VEC, NV>(xr[u], x);
-      unpack_row<T, VEC, NV>(zr[u], z);
-      const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
-      if constexpr (!kKeep) affine();
-      if (a.z) {
-        if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, true>(x, z, w, b, rstd);
-        else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, true>(x, z, w, b, rstd);
-        else finish<GDR_ACT_NONE, true>(x, z, w, b, rstd);
-      } else {
-        if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, false>(x, z, w, b, rstd);
-        else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, false>(x, z, w, b, rstd);
-        else finish<GDR_ACT_NONE, false>(x, z, w, b, rstd);
-      }
+  const long long first = p.first_row(blockIdx.x, slot, kPerBlock, a.G);
+  const int mine = p.count(p.used(blockIdx.x, slot, kPerBlock), first, a.rows);
+  const long long off = (long long)g * a.D + lane * VEC, dense = (long long)a.G * a.D;
+  const T *xp = static_cast<const T *>(a.x) + off + first * a.x_stride;  // the row asked for next
+  const T *zp = static_cast<const T *>(a.z) + off + first * a.z_stride;
+  T *yp = static_cast<T *>(a.y) + off + first * dense;
+  const long long x_step = p.step * a.x_stride, z_step = p.step * a.z_stride;
+
+  constexpr bool kQueue = norm_queue<T, VEC, NV>;
+  constexpr int kStages = NV == 1 ? 4 : 3;
+  constexpr int kWaiting = kQueue ? 2 * NV : 1;
+  __shared__ Raw<T, VEC> waiting[kQueue ? kStages : 1][kWaiting][kRowThreads];
+  Queue<Raw<T, VEC>, kWaiting, kStages> queue{waiting};
+  const auto ask = [&](int turn, int stage) {
+    if (turn < mine) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (row < last && in[i])
-          store_access<T, VEC>(yp + row * a.G * a.D + i * L * VEC, x, i);
+        if (in[i]) {
+          queue.request(stage, i, xp + i * L * VEC);
+          if (a.z) queue.request(stage, NV + i, zp + i * L * VEC);
+        }
     }
+    queue.commit();
+    xp += x_step;
+    zp += z_step;
+  };
+  if constexpr (kQueue) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ask(i, i);
+  }
+  int stage = 0;
+  for (int k = 0; k < p.turns; ++k, yp += p.step * dense) {
+    const bool live = k < mine;
+    Raw<T, VEC> xr[NV], zr[NV];
+    if constexpr (kQueue) {
+      ask(k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      queue.wait();
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xr[i] = zr[i] = Raw<T, VEC>{};
+      if (!live || !in[i]) continue;
+      if constexpr (kQueue) {
+        xr[i] = queue.get(stage, i);
+        if (a.z) zr[i] = queue.get(stage, NV + i);
+      } else {
+        xr[i] = load_raw<T, VEC>(xp + i * L * VEC);
+        if (a.z) zr[i] = load_raw<T, VEC>(zp + i * L * VEC);
+      }
+    }
+    if constexpr (kQueue) {
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      xp += x_step;
+      zp += z_step;
+    }
+    float2 x[N], z[N];
+    unpack_row<T, VEC, NV>(xr, x);
+    unpack_row<T, VEC, NV>(zr, z);
+    const float rstd = normalise<VEC, L, NV>(x, in, a.center, inv_d, a.eps);
+    if constexpr (!kKeep) affine();
+    if (a.z) {
+      if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, true>(x, z, w, b, rstd);
+      else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, true>(x, z, w, b, rstd);
+      else finish<GDR_ACT_NONE, true>(x, z, w, b, rstd);
+    } else {
+      if (a.act == GDR_ACT_SILU) finish<GDR_ACT_SILU, false>(x, z, w, b, rstd);
+      else if (a.act == GDR_ACT_SIGMOID) finish<GDR_ACT_SIGMOID, false>(x, z, w, b, rstd);
+      else finish<GDR_ACT_NONE, false>(x, z, w, b, rstd);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (live && in[i]) store_access<T, VEC>(yp + i * L * VEC, x, i);
   }
 }
 

@@ -20,6 +20,7 @@ struct RowPlan {
   int by_block;
   int sum;  // whether partial rows are left for a second launch
   long long step;
+  int turns;  // rows of a slot at most
 
   __device__ __forceinline__ int group(int block, int slot_in_block, int per_block, int G) const {
     return (unsigned)(by_block ? block : block * per_block + slot_in_block) % (unsigned)G;
@@ -32,6 +33,11 @@ struct RowPlan {
   __device__ __forceinline__ bool used(int block, int slot_in_block, int per_block) const {
     return by_block || block * per_block + slot_in_block < slots;
   }
+  // The rows of a slot: row `first` and those every `step` after it.  (Only the last turn's can
+  // lie behind the end.)
+  __device__ __forceinline__ int count(bool used, long long first, long long rows) const {
+    return used ? turns - (first + (turns - 1) * step >= rows) : 0;
+  }
 };
 
 // A plan in which a slot takes about `turns` rows, and at least `least_blocks`
@@ -42,8 +48,12 @@ inline RowPlan row_plan(long long rows, int G, int per_block, int turns, int lea
                                    : (rows * G + per_block - 1) / per_block;  // a row a slot
   const long long every = by_block ? G : ((long long)G + per_block - 1) / per_block;
   long long blocks = (whole + turns - 1) / turns;
-  if (blocks < least_blocks) blocks = whole < least_blocks ? whole : least_blocks;
-  if (by_block) blocks = (blocks + G - 1) / G * G;
+  if (blocks < least_blocks) {
+    blocks = whole < least_blocks ? whole : least_blocks;
+    if (by_block) blocks = blocks / G * G;  // (not one block more than fit at once)
+  } else if (by_block) {
+    blocks = (blocks + G - 1) / G * G;
+  }
   if (blocks < every) blocks = every;  // every group once
   if (blocks > 1 << 24) blocks = by_block ? (1 << 24) / G * G : 1 << 24;  // (32-bit slots)
   RowPlan p;
@@ -52,6 +62,7 @@ inline RowPlan row_plan(long long rows, int G, int per_block, int turns, int lea
   p.sum = 0;
   p.step = by_block ? blocks / G * per_block : blocks * per_block / G;
   p.slots = by_block ? 0 : (int)(p.step * G);
+  p.turns = (int)((rows + p.step - 1) / p.step);
   return p;
 }
 
@@ -131,16 +142,19 @@ __device__ __forceinline__ void store_access(T *p, const float2 (&x)[N], int i) 
   store_vec<T, VEC>(p, v);
 }
 
-// A thread's own queue of 16-byte loads in shared memory, STAGES rows of TENSORS
-// accesses: more bytes in flight than registers have room for.  Only the thread
-// that asked for them reads them, so nothing waits at a barrier.
-template <int TENSORS, int STAGES>
+// A thread's own queue of loads of R (8 or 16 bytes) in shared memory, STAGES
+// rows of N accesses: more bytes in flight than registers have room for.  Only
+// the thread that asked for them reads them, so nothing waits at a barrier.
+template <typename R, int N, int STAGES>
 struct Queue {
-  uint4 (*buf)[TENSORS][kRowThreads];  // [STAGES] in shared memory
+  R (*buf)[N][kRowThreads];  // [STAGES] in shared memory
 
-  __device__ __forceinline__ void request(int stage, int tensor, const void *p) {
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&buf[stage][tensor][threadIdx.x]);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+  __device__ __forceinline__ void request(int stage, int i, const void *p) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&buf[stage][i][threadIdx.x]);
+    if constexpr (sizeof(R) == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p) : "memory");
   }
   // Ends a row's requests (also of a row that has none).
   __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -148,9 +162,7 @@ struct Queue {
   __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
   }
-  __device__ __forceinline__ uint4 get(int stage, int tensor) const {
-    return buf[stage][tensor][threadIdx.x];
-  }
+  __device__ __forceinline__ R get(int stage, int i) const { return buf[stage][i][threadIdx.x]; }
 };
 
 // The sum over the L lanes (a power of two) that share a row, in all of them.
