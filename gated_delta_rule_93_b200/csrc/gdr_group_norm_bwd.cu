@@ -216,12 +216,15 @@ __global__ void __launch_bounds__(1024) group_norm_sum_kernel(const float *part,
     sum_columns(part + (blockIdx.y ? (size_t)rows * cols : 0), rows, cols, out, blockIdx.x);
 }
 
-constexpr int kTurns = 16;
-constexpr int kFewTurns = 4;  // rows a slot takes rather than have a second launch
+constexpr int kTurns = 16;        // rows of a lane in a block, more where that makes more than
+constexpr int kMostBlocks = 8192;  // these blocks (each leaves a partial row to add up)
+constexpr int kFewTurns = 4;       // rows a slot takes rather than have a second launch
 
 RowPlan bwd_plan(long long rows, int G, int lanes, int per_sm, int per_channel) {
   const int per_block = kRowThreads / lanes;
-  RowPlan p = row_plan(rows, G, per_block, kTurns, kSMs * per_sm, per_channel);
+  const long long most = rows * G / ((long long)kMostBlocks * per_block);
+  const int turns = most > kTurns ? (int)(most < (1 << 30) ? most : 1 << 30) : kTurns;
+  RowPlan p = row_plan(rows, G, per_block, turns, kSMs * per_sm, per_channel);
   // few rows: as few blocks as have every channel once
   if (per_channel ? rows <= kFewTurns * per_block : rows * G <= kFewTurns * per_block)
     p = row_plan(rows, G, per_block, kFewTurns, 1, per_channel);

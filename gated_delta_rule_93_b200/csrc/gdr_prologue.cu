@@ -23,6 +23,7 @@ namespace {
 constexpr float kNormEps = 1e-6f;
 constexpr int kNormTurns = 4, kNormBlocks = 4 * kSMs;
 constexpr int kGateTurns = 8, kGateBlocks = 4 * kSMs;
+constexpr int kMostParts = 4096;  // partial sums of a head at most
 
 // The gates' blocks: `heads` heads of `tokens` tokens at a time; blocks that
 // share a tile of heads are `step` tokens apart.
@@ -50,7 +51,7 @@ GatePlan gate_plan(long long tokens, int H, int dk, int per_channel) {
   const int least = (kGateBlocks + p.tiles - 1) / p.tiles;
   if (rows < least) rows = passes < least ? passes : least;
   if (rows < 1) rows = 1;
-  if (rows > (1 << 24) / p.tiles) rows = (1 << 24) / p.tiles;
+  if (rows > kMostParts) rows = kMostParts;
   p.blocks = (int)(rows * p.tiles);
   p.step = rows * p.tokens;
   return p;

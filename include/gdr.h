@@ -499,7 +499,7 @@ typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 } gdr_act
  *
  * 1 <= D <= 1024, G * D <= 65536.  Pointers aligned to their element; calls
  * whose pointers, strides and D are multiples of 16 bytes run fastest.  y may
- * be x (dense).  fp32 statistics; one launch, no workspace.
+ * be x (dense), but overlap nothing else.  fp32 statistics; one launch, no workspace.
  */
 gdr_status gdr_group_norm_fwd(const void *x, const void *z, gdr_dtype dtype, long long x_stride,
                               long long z_stride, const float *weight, const float *bias,
@@ -516,8 +516,9 @@ gdr_status gdr_group_norm_fwd(const void *x, const void *z, gdr_dtype dtype, lon
  * The statistics are computed again from x.  Sums over rows run in a fixed
  * order (the same call gives the same bits).  dweight / dbias need
  * gdr_group_norm_bwd_workspace_bytes of workspace (16-byte aligned; calls
- * that overlap on the GPU need one each); two launches with them, else one.
- * dz needs z.
+ * that overlap on the GPU need one each); two launches with them (one where a
+ * block has all rows of its channels), else one.  dz needs z.  Outputs may
+ * not overlap inputs.
  */
 size_t gdr_group_norm_bwd_workspace_bytes(long long rows, int G, int D, gdr_dtype dtype,
                                           int per_channel);
@@ -543,7 +544,8 @@ gdr_status gdr_group_norm_bwd(const void *dy, const void *x, const void *z, gdr_
  *
  * qn, kn, g, beta are the inputs of gdr_chunk_fwd and gdr_chunk_bwd (with
  * tokens = B * T).  dk in {32, 64, 128}, H a multiple of Hk, pointers 16-byte
- * aligned, strides multiples of 16 bytes.  One launch, no workspace.
+ * aligned, strides multiples of 16 bytes.  One launch, no workspace; outputs
+ * may not overlap inputs.
  */
 gdr_status gdr_prologue_fwd(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
                             long long k_stride, const float *a, gdr_gate_kind gate,
@@ -563,7 +565,8 @@ gdr_status gdr_prologue_fwd(const void *q, const void *k, gdr_dtype in_dtype, lo
  *
  * The rounding of qn, kn to in_dtype counts as the identity.  Needs
  * gdr_prologue_bwd_workspace_bytes of workspace (16-byte aligned; calls that
- * overlap on the GPU need one each); two launches.
+ * overlap on the GPU need one each); at most two launches.  Outputs may not
+ * overlap inputs.
  */
 size_t gdr_prologue_bwd_workspace_bytes(long long tokens, int H, int dk, gdr_gate_kind gate);
 gdr_status gdr_prologue_bwd(const void *q, const void *k, gdr_dtype in_dtype, long long q_stride,
