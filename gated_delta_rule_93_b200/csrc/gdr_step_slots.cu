@@ -6,25 +6,36 @@
 // S' = S Diag(alpha):
 //     p_i = S'_i . k,  r_i = S'_i . q,  u_i = beta (v_i - p_i)
 //     S_i <- S'_i + u_i k^T,  o_i = r_i + u_i (k . q)
-// Rows are independent, so a thread block takes 64 rows of one (request,
-// value head; 32 where dv is 32), reads them once, runs the request's tokens with the rows in
-// registers and writes them wherever the request keeps a state.  One token a
-// request moves 2 * 4 * dk * dv bytes per (request, head) for 7 dk dv flops:
-// bound by HBM.
+// Rows are independent, so a block takes some rows of one (request, value
+// head), reads them once, runs the request's tokens with the rows in registers
+// and writes them wherever the request keeps a state.  One token a request moves
+// 2 * 4 * dk * dv bytes per (request, head) for 7 dk dv flops: bound by HBM.  Two
+// kernels, by whether the call has cu_seqlens:
 //
-// Layout: 8 lanes share a row, lane l of them holding the float4s at columns
-// 32 c + 4 l: a warp's load is four whole 128-byte lines, and a row's two dot
-// products need 3 shuffle steps instead of 5.  What all rows of a head share (k, q
-// with their norms, the gates, k . q) is prepared once per block in shared
-// memory, 8 tokens at a time, a warp each: the first 8 while the state's loads are in flight.
+// One token a request: a warp for 8 rows that prepares k, q and the gate for
+// itself, no shared memory, no barrier.  256 requests x 16 heads of 128 x 128:
+// 83.1 us, 6508 GB/s (a copy runs at 6456); with the preparation shared by a block,
+// whose warps then load, wait and store in step, 90 to 95 us.
+//
+// Several tokens: a block of 4 warps takes 64 rows (2 warps, 32 rows, where dv is
+// 32), and what all rows of a head share (k, q with their norms, the gates, k . q)
+// is prepared once per block in shared memory, 8 tokens at a time, two a warp.
+// 8 lanes share a row, lane l of them holding the float4s at columns 32 c + 4 l (a
+// warp's load is four whole 128-byte lines), and a lane has 4 rows, so that the
+// shared k and q are read once for 4 rows and a row's two dot products cost 7/4
+// shuffles.  48 requests of 1 to 5 tokens, 32 heads of 128 x 128, every state kept:
+// 65.1 us, 6144 GB/s; 64 requests of 1 to 4 tokens, 16 heads, one state kept: 26.9 us
+// (2 rows a lane in blocks of 8 warps: 71.2 and 36.1 us).  Long requests run at about
+// 0.6 us a token (8 requests x 16 heads), bound by the instructions and the latency of
+// one token after the other: from 16 tokens on the chunked forward is faster there.
 #include "gdr_rows.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kRpt = 4;                 // rows per thread, 4 apart
-constexpr int kWarpRows = 4 * kRpt;      // rows of a warp
-constexpr int kTokens = 8;               // tokens prepared at a time
+constexpr int kRpt = 4;             // rows of a lane, 4 apart
+constexpr int kWarpRows = 4 * kRpt;  // rows of a warp
+constexpr int kTokens = 8;           // tokens prepared at a time
 constexpr int rows_of(int warps) { return kWarpRows * warps; }  // of a block
 
 constexpr float kNormEps = 1e-6f;
@@ -45,6 +56,12 @@ __device__ __forceinline__ void load_lane(const void *p, size_t i, float (&x)[VE
   if constexpr (!BF16 && VEC == 4) {
     const float4 t = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
     x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+  } else if constexpr (!BF16 && VEC == 2) {
+    const float2 t = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
+    x[0] = t.x; x[1] = t.y;
+  } else if constexpr (BF16 && VEC == 2) {
+    const unsigned t = *reinterpret_cast<const unsigned *>(static_cast<const __nv_bfloat16 *>(p) + i);
+    x[0] = __uint_as_float(t << 16); x[1] = __uint_as_float(t & 0xffff0000u);
   } else if constexpr (BF16 && VEC == 4) {
     const uint2 t = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
     x[0] = __uint_as_float(t.x << 16); x[1] = __uint_as_float(t.x & 0xffff0000u);
@@ -53,6 +70,15 @@ __device__ __forceinline__ void load_lane(const void *p, size_t i, float (&x)[VE
 #pragma unroll
     for (int e = 0; e < VEC; ++e) x[e] = load_in(p, i + e, BF16);
   }
+}
+template <int VEC>
+__device__ __forceinline__ void store_lane(float *p, const float (&x)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else if constexpr (VEC == 2)
+    *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+  else
+    p[0] = x[0];
 }
 template <int VEC>
 __device__ __forceinline__ void load_lane_stream(const float *p, float (&x)[VEC]) {
@@ -82,40 +108,26 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Sum NV per-lane values over groups of 8 lanes, halving the values while the
-// lane masks allow it: afterwards a lane holds the sum of value (lane & 7) >> SH,
-// NV = 8 >> SH.
-template <int NV>
-__device__ __forceinline__ float reduce8(float (&x)[NV], int lane) {
-  static_assert(NV == 2 || NV == 4 || NV == 8);
-  int n = NV;
+// Sums 8 per-lane values over groups of 8 lanes, halving the values each
+// time: lane l ends up with the sum of value l & 7.
+__device__ __forceinline__ float reduce8(float (&x)[8], int lane) {
 #pragma unroll
-  for (int m = 4; m; m >>= 1) {
-    if (n > 1) {
-      n >>= 1;
+  for (int m = 4; m; m >>= 1)
 #pragma unroll
-      for (int i = 0; i < NV / 2; ++i) {
-        if (i < n) {
-          const bool hi = lane & m;
-          const float send = hi ? x[i] : x[i + n];
-          const float keep = hi ? x[i + n] : x[i];
-          x[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-        }
-      }
-    } else {
-      x[0] += __shfl_xor_sync(0xffffffffu, x[0], m);
+    for (int i = 0; i < m; ++i) {
+      const bool hi = lane & m;
+      const float send = hi ? x[i] : x[i + m];
+      const float keep = hi ? x[i + m] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
     }
-  }
   return x[0];
 }
 
 template <int DK, int WARPS, bool BF16, bool PERCH>
 __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 32) / WARPS)
     gdr_step_slots_kernel(StepSlotsArgs a) {
-  constexpr int RPT = kRpt, kRows = rows_of(WARPS);
+  constexpr int kRows = rows_of(WARPS);
   constexpr int NC = DK / 32;  // float4s of a row per lane
-  constexpr int NV = 2 * RPT;  // dot products per thread
-  constexpr int SH = NV == 8 ? 0 : NV == 4 ? 1 : 2;
   __shared__ Prepared<DK, WARPS, PERCH> sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks_per_head = a.dv / kRows;
@@ -127,11 +139,8 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
   const int row0 = block_row + in_block;
   const int col0 = (lane & 7) * 4;
 
-  int t0 = r, t1 = r + 1;
-  if (a.cu) {
-    t0 = min(max(a.cu[r], 0), a.total);
-    t1 = min(max(a.cu[r + 1], t0), a.total);
-  }
+  const int t0 = min(max(a.cu[r], 0), a.total);
+  const int t1 = min(max(a.cu[r + 1], t0), a.total);
   const int src = a.src[r];
   if (t0 >= t1 || src == GDR_SLOT_SKIP) return;
   if (src < GDR_SLOT_ZERO || src >= a.slots) {
@@ -140,11 +149,11 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
   }
   const size_t in_slot = ((size_t)h * a.dv + row0) * DK + col0;
 
-  float2 s[RPT][2 * NC];
+  float2 s[kRpt][2 * NC];
   if (src >= 0) {
     const float *p = a.pool + (size_t)src * a.slot_stride + in_slot;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+    for (int i = 0; i < kRpt; ++i)
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + i * 4 * DK + c * 32));
@@ -153,7 +162,7 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
       }
   } else {
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+    for (int i = 0; i < kRpt; ++i)
 #pragma unroll
       for (int c = 0; c < 2 * NC; ++c) s[i][c] = make_float2(0.f, 0.f);
   }
@@ -164,20 +173,18 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
     for (int j = warp; j < n; j += WARPS) {  // a token a warp, DK / 32 channels a lane
       const size_t t = tb + j, th = t * a.H + h;
       float kv[NC], qv[NC], gv[PERCH ? NC : 1];
-#pragma unroll
-      for (int e = 0; e < NC; ++e) {
-        kv[e] = load_in(a.k, t * a.k_stride + (size_t)hk * DK + lane + 32 * e, BF16);
-        qv[e] = load_in(a.q, t * a.q_stride + (size_t)hk * DK + lane + 32 * e, BF16);
-        if constexpr (PERCH) gv[e] = a.g[th * DK + lane + 32 * e];
-      }
-      if constexpr (!PERCH) gv[0] = a.g[th];
+      load_lane<NC, BF16>(a.k, t * a.k_stride + (size_t)hk * DK + lane * NC, kv);
+      load_lane<NC, BF16>(a.q, t * a.q_stride + (size_t)hk * DK + lane * NC, qv);
+      if constexpr (PERCH)
+        load_lane<NC, false>(a.g, th * DK + lane * NC, gv);
+      else
+        gv[0] = a.g[th];
       const float bl = a.beta[th];
       // where the state goes after this token (-1: nowhere)
       int d = a.dst ? a.dst[t] : ((int)t == t1 - 1 ? src : -1);
-#pragma unroll
-      for (int e = 0; e < kRows / 32; ++e)
-        sm.v[j][lane + 32 * e] =
-            load_in(a.v, t * a.v_stride + (size_t)h * a.dv + block_row + lane + 32 * e, BF16);
+      float vv[kRows / 32];
+      load_lane<kRows / 32, BF16>(
+          a.v, t * a.v_stride + (size_t)h * a.dv + block_row + lane * (kRows / 32), vv);
       const float scale = a.gate_scale ? a.gate_scale[h] : 0.f;
       float kk = 0.f, qq = 0.f, kq = 0.f, rk = 1.f, rq = 1.f;
 #pragma unroll
@@ -191,11 +198,15 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
       if (a.norm_qk & GDR_NORM_Q) rq = rsqrtf(warp_sum(qq) + kNormEps);
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        sm.k[j][lane + 32 * e] = kv[e] * rk;
-        sm.q[j][lane + 32 * e] = qv[e] * rq;
+        kv[e] *= rk;
+        qv[e] *= rq;
         if constexpr (PERCH)
-          sm.al[j][lane + 32 * e] = expf(a.gate_scale ? -scale * softplus(gv[e]) : gv[e]);
+          gv[e] = expf(a.gate_scale ? -scale * softplus(gv[e]) : gv[e]);
       }
+      store_lane<NC>(&sm.k[j][lane * NC], kv);
+      store_lane<NC>(&sm.q[j][lane * NC], qv);
+      if constexpr (PERCH) store_lane<NC>(&sm.al[j][lane * NC], gv);
+      store_lane<kRows / 32>(&sm.v[j][lane * (kRows / 32)], vv);
       if (lane == 0) {
         if constexpr (!PERCH)
           sm.al[j][0] = expf(a.gate_scale ? -scale * softplus(gv[0]) : gv[0]);
@@ -211,10 +222,11 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
     __syncthreads();
     for (int j = 0; j < n; ++j) {
       const size_t to = ((size_t)(tb + j) * a.H + h) * a.dv;
-      const int idx = (lane & 7) >> SH;   // the dot product this lane ends up with
-      const int mine = idx % RPT;         // its row: p for idx < RPT, r after
+      // the dot product this lane ends up with: p of row `mine` on lanes 0-3 of 8, r on 4-7
+      const int mine = lane & 3;
+      const bool is_p = !(lane & 4);
       const float v = sm.v[j][in_block + 4 * mine];
-      float2 p2[RPT] = {}, r2[RPT] = {}, kr[2 * NC];
+      float2 p2[kRpt] = {}, r2[kRpt] = {}, kr[2 * NC];
       float2 al = both(0.f);
       if constexpr (!PERCH) al = both(sm.al[j][0]);
 #pragma unroll
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
           const float2 q2 = half ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
           if constexpr (PERCH) al = half ? make_float2(a4.z, a4.w) : make_float2(a4.x, a4.y);
 #pragma unroll
-          for (int i = 0; i < RPT; ++i) {
+          for (int i = 0; i < kRpt; ++i) {
             float2 &x = s[i][2 * c + half];
             x = mul2(x, al);  // decay first
             p2[i] = fma2(x, k2, p2[i]);
@@ -238,33 +250,33 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
           }
         }
       }
-      float part[NV];
+      float part[2 * kRpt];
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) {
+      for (int i = 0; i < kRpt; ++i) {
         part[i] = p2[i].x + p2[i].y;
-        part[RPT + i] = r2[i].x + r2[i].y;
+        part[kRpt + i] = r2[i].x + r2[i].y;
       }
-      const float red = reduce8<NV>(part, lane);
-      const float u_mine = sm.beta[j] * (v - red);  // meaningful where idx < RPT
-      float u[RPT], um = 0.f;
+      const float red = reduce8(part, lane);
+      const float u_mine = sm.beta[j] * (v - red);  // meaningful where is_p
+      float u[kRpt], um = 0.f;
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) {
-        u[i] = __shfl_sync(0xffffffffu, u_mine, (lane & 24) + (i << SH));
+      for (int i = 0; i < kRpt; ++i) {
+        u[i] = __shfl_sync(0xffffffffu, u_mine, (lane & 24) + i);
         if (i == mine) um = u[i];
       }
-      if (idx >= RPT && (lane & ((1 << SH) - 1)) == 0)
+      if (!is_p)
         store_out(a.o, to + row0 + 4 * mine, red + um * sm.kq[j], BF16);
       const int d = sm.dst[j];
 #pragma unroll
       for (int c = 0; c < 2 * NC; ++c)
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) s[i][c] = fma2(both(u[i]), kr[c], s[i][c]);
+        for (int i = 0; i < kRpt; ++i) s[i][c] = fma2(both(u[i]), kr[c], s[i][c]);
       if (d >= 0) {
         float *out = a.pool + (size_t)d * a.slot_stride + in_slot;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int i = 0; i < RPT; ++i)
+          for (int i = 0; i < kRpt; ++i)
             __stcs(reinterpret_cast<float4 *>(out + i * 4 * DK + c * 32),
                    make_float4(s[i][2 * c].x, s[i][2 * c].y, s[i][2 * c + 1].x, s[i][2 * c + 1].y));
       }
