@@ -9,18 +9,27 @@
 //
 // L lanes hold one key head of one token in registers (16-byte accesses), so
 // every tensor is read once and written once: bound by HBM, with the loads of
-// U tokens of q and k requested before the first is used.  The gates are the work
-// of other blocks of the same launch: a thread for a (token, head) with a
-// scalar gate, dk / 4 lanes with a per-channel one.  Every slot keeps its head
-// for all its tokens (no division in the loops), so ds adds up in registers
-// and then over the block; a second launch adds the blocks' sums in a fixed
-// order, unless one block had all tokens.
+// two tokens of q and k requested before the first is used, and blocks of 4 tokens
+// a slot so that the SMs finish together.  The gates are the work of other blocks
+// of the same launch: a thread for a (token, head) with a scalar gate, dk / 4
+// lanes with a per-channel one.  Every slot keeps its head for all its tokens (no
+// division in the loops: 115 us with them, 70 us without, where it is 65 us now), so ds
+// adds up in registers and then over the block; a second launch adds the blocks'
+// sums in a fixed order, unless one block had all tokens.
+//
+// 32768 tokens, bf16, scalar gates, 8 key heads of 128 for 16 value heads: forward
+// 64.8 us (6347 GB/s; a copy runs at 6456), gradient 128.7 us (6353 GB/s).
+// Per-channel gates spend a third of their time on softplus and sigmoid: 8192
+// tokens x 16 x 128 forward 48.8 us (5521 GB/s), gradient 83.3 us (5659 GB/s).  The
+// gradient takes q, then k, so that 64 registers do and four blocks fit an SM (both
+// at once, three blocks: 131.1 and 91.0 us).
 #include "gdr_rows.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr float kNormEps = 1e-6f;
+// Tokens of a slot in a block, or fewer where that leaves less than so many blocks.
 constexpr int kNormTurns = 4, kNormBlocks = 4 * kSMs;
 constexpr int kGateTurns = 8, kGateBlocks = 4 * kSMs;
 constexpr int kMostParts = 4096;  // partial sums of a head at most
@@ -45,7 +54,6 @@ GatePlan gate_plan(long long tokens, int H, int dk, int per_channel) {
   p.heads = per_channel ? 1 : H < slots ? H : slots;
   p.tiles = (H + p.heads - 1) / p.heads;
   p.tokens = slots / p.heads;
-  // a slot takes kGateTurns tokens, or fewer where that leaves less than kGateBlocks blocks
   const long long passes = (tokens + p.tokens - 1) / p.tokens;
   long long rows = (passes + kGateTurns - 1) / kGateTurns;
   const int least = (kGateBlocks + p.tiles - 1) / p.tiles;
@@ -279,12 +287,6 @@ __global__ void __launch_bounds__(kRowThreads, 4) prologue_bwd_kernel(PrologueAr
   }
 }
 
-__global__ void __launch_bounds__(1024) prologue_sum_kernel(const float *part, int rows, int cols,
-                                                            float *out) {
-  after_previous();
-  sum_columns(part, rows, cols, out, blockIdx.x);
-}
-
 template <bool BWD, typename T, int VEC, int L>
 cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
   const Split p = {row_plan(a.tokens, a.Hk, kRowThreads / L, kNormTurns, kNormBlocks, false),
@@ -297,8 +299,7 @@ cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
     if (p.gate.blocks > p.gate.tiles) {
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      return launch_next(prologue_sum_kernel, dim3((a.H + sum_width(a.H) - 1) / sum_width(a.H)), 1024,
-                         stream, a.ws, p.gate.blocks / p.gate.tiles, a.H, a.dgate_scale);
+      return launch_sums(a.ws, p.gate.blocks / p.gate.tiles, a.H, a.dgate_scale, nullptr, stream);
     }
   }
   return cudaGetLastError();

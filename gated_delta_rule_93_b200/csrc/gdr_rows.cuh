@@ -2,6 +2,8 @@
 // elements, sums over the lanes that share a row, sums of partial rows.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "gdr_internal.cuh"
 
 namespace gdr {
@@ -268,33 +270,68 @@ __device__ __forceinline__ void let_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// out[c] = sum over k of part[k * cols + c], in a fixed order.  A block of 1024
-// threads takes W columns (32 bytes of a row, or 16 of a short one) and adds up
-// in a tree.
-__host__ __device__ __forceinline__ int sum_width(int cols) {
-  return cols <= 4 ? 4 : 8;
-}
-__device__ __forceinline__ void sum_columns(const float *part, int rows, int cols, float *out,
-                                            int block) {
-  __shared__ float s[1024];
-  const int W = sum_width(cols), Y = 1024 / W;
-  const int x = threadIdx.x % W, y = threadIdx.x / W;
-  const int c = block * W + x;
+// out[c] = sum over k of part[k * cols + c], in a fixed order.  A block takes
+// kSumWidth columns (32 bytes of a row), a thread every kSumRows-th row of one;
+// they add up in a tree.  Many rows are shared by a cluster of kSumParts blocks, whose
+// first adds up their sums (2048 rows of 128 columns: 3.3 us less than with one block of
+// 1024 threads for 8 columns).
+constexpr int kSumThreads = 256, kSumWidth = 8, kSumRows = kSumThreads / kSumWidth;
+constexpr int kSumParts = 8, kSumManyRows = 4 * kSumRows;
+
+template <int PARTS>
+__device__ __forceinline__ void sum_columns(const float *part, int rows, int cols, float *out) {
+  __shared__ float s[kSumThreads];
+  const int x = threadIdx.x % kSumWidth, y = threadIdx.x / kSumWidth;
+  const int rank = blockIdx.x % PARTS, c = blockIdx.x / PARTS * kSumWidth + x;
+  const int step = PARTS * kSumRows;
   float v[4] = {};
   if (c < cols) {
-    int k = y;
-    for (; k + 3 * Y < rows; k += 4 * Y)
+    int k = rank * kSumRows + y;
+    for (; k + 3 * step < rows; k += 4 * step)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += part[(size_t)(k + i * Y) * cols + c];
-    for (; k < rows; k += Y) v[0] += part[(size_t)k * cols + c];
+      for (int i = 0; i < 4; ++i) v[i] += part[(size_t)(k + i * step) * cols + c];
+    for (; k < rows; k += step) v[0] += part[(size_t)k * cols + c];
   }
   s[threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
-  for (int n = 512; n >= W; n >>= 1) {
+#pragma unroll
+  for (int n = kSumThreads / 2; n >= kSumWidth; n >>= 1) {
     if ((int)threadIdx.x < n) s[threadIdx.x] += s[threadIdx.x + n];
     __syncthreads();
   }
-  if ((int)threadIdx.x < W && c < cols) out[c] = s[threadIdx.x];
+  if constexpr (PARTS > 1) {
+    const auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    if (rank == 0 && (int)threadIdx.x < kSumWidth && c < cols) {
+      float sum = s[x];
+#pragma unroll
+      for (int r = 1; r < PARTS; ++r) sum += *cluster.map_shared_rank(&s[x], r);
+      out[c] = sum;
+    }
+    cluster.sync();  // (a block's sums stay until they are read)
+  } else if ((int)threadIdx.x < kSumWidth && c < cols) {
+    out[c] = s[threadIdx.x];
+  }
+}
+
+// Columns of `a` from the first `rows` partial rows, and of `b`, where there is one, from the
+// next `rows` (the second half of the grid's y).
+template <int PARTS>
+__global__ void __launch_bounds__(kSumThreads) __cluster_dims__(PARTS, 1, 1)
+    sum_kernel(const float *part, int rows, int cols, float *a, float *b) {
+  after_previous();
+  float *out = blockIdx.y ? b : a;
+  if (out) sum_columns<PARTS>(part + (blockIdx.y ? (size_t)rows * cols : 0), rows, cols, out);
+}
+
+inline cudaError_t launch_sums(const float *part, int rows, int cols, float *a, float *b,
+                               cudaStream_t stream) {
+  const int blocks = (cols + kSumWidth - 1) / kSumWidth;
+  if (rows > kSumManyRows)
+    return launch_next(sum_kernel<kSumParts>, dim3(blocks * kSumParts, b ? 2 : 1), kSumThreads, stream,
+                       part, rows, cols, a, b);
+  return launch_next(sum_kernel<1>, dim3(blocks, b ? 2 : 1), kSumThreads, stream, part, rows, cols, a,
+                     b);
 }
 
 }  // namespace gdr

@@ -1,11 +1,11 @@
 // Torch front end of the operators around the mixer (see include/gdr.h).
 //
 // A decode loop calls these operators once per layer and token, and their
-// kernels take a few microseconds: checking a dozen tensors and marshalling
-// two dozen arguments in Python took 9 us a call on the host (3 us more for an output),
-// the launch itself 4.  So this part is compiled: it looks at the tensors, allocates
-// what the caller did not pass, and calls the C ABI with raw pointers.  It
-// holds no arithmetic and no state but the ABI's addresses.
+// kernels take a few microseconds.  Checks, allocation and marshalling in Python
+// took 12 us a call beside the launch's 4 (pooled step); here they take about 2, so this
+// part is compiled: it looks at the tensors, allocates what the caller did not
+// pass, and calls the C ABI with raw pointers.  It holds no arithmetic and no
+// state but the ABI's addresses.
 //
 // The functions take every argument by position (binding.py gives them names,
 // defaults and documentation) and return the status of the ABI call as an int
