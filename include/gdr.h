@@ -24,7 +24,9 @@
  * - Every pointer is a CUDA device pointer owned by the caller.  The library
  *   allocates no device memory in any call and keeps no per-call state.
  * - All device work is enqueued on `stream` (a cudaStream_t; NULL means the
- *   legacy default stream) and runs asynchronously.
+ *   legacy default stream) and runs asynchronously.  The first call of an
+ *   entry point on a device looks addresses up and loads its kernels: make it
+ *   before any stream capture.
  * - Argument errors are detected on the host, before anything is enqueued:
  *   the call returns GDR_ERR_INVALID_ARG or GDR_ERR_UNSUPPORTED and launches
  *   nothing; gdr_last_error_message() then describes the problem.

@@ -116,6 +116,40 @@ def test_ragged_requests_keep_every_state(cuda_device, dtype, gate, fused):
     close(d["pool"], rp, tolerance(128, 9), "pool")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate", ["scalar", "channel"])
+@pytest.mark.parametrize("dk", [32, 64, 128])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+def test_head_dims_with_several_tokens(cuda_device, dtype, gate, dk, dv):
+    """Every head size, three value heads to a key head, over the 8 tokens that are
+    prepared at a time."""
+    lens = [2, 11, 1]
+    d = make(lens, 1, 3, dk, dv, dtype, gate, True, seed=dk * dv, slots=16)
+    src, dst = i32([15, SLOT_ZERO, 1]), i32([0, 2, *[-1] * 9, 3, 4, 5])
+    ro, rp = expect(d, src, dst)
+    o = call(d, src, dst)
+    torch.cuda.synchronize()
+    close(o, ro, tolerance(dk, 11, dtype), "o")
+    close(d["pool"], rp, tolerance(dk, 11), "pool")
+
+
+@pytest.mark.parametrize("gate", ["scalar", "channel"])
+@pytest.mark.parametrize("cu", [True, False])
+def test_nan_and_infinities_stay_with_their_request(cuda_device, gate, cu):
+    """A NaN key, an infinite value and a slot full of NaN reach their own request's
+    output and state only; a new request does not read what its slot held."""
+    d = make([1] * 4, 1, 2, 64, 64, torch.float32, gate, slots=8, seed=21)
+    src, dst = i32([0, 1, 2, SLOT_ZERO]), i32([0, 1, 2, 3])
+    clean = dict(d, pool=d["pool"].clone())
+    want = call(clean, src, dst, cu=cu)
+    d["k"][0], d["v"][1], d["pool"][2], d["pool"][3] = (float("nan"), float("inf"), float("nan"),
+                                                        float("nan"))
+    o = call(d, src, dst, cu=cu)
+    torch.cuda.synchronize()
+    assert torch.isnan(o[0]).all() and not torch.isfinite(o[1]).all() and torch.isnan(o[2]).all()
+    assert torch.equal(o[3], want[3]) and torch.equal(d["pool"][3:], clean["pool"][3:])
+
+
 @pytest.mark.parametrize("tokens", [1, 4, 5, 301])
 def test_long_requests_without_dst(cuda_device, tokens):
     """dst None: the last state goes back to the slot it came from."""
