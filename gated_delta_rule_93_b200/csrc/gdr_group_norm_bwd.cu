@@ -54,6 +54,8 @@ __device__ __forceinline__ float gradients(float2 (&x)[N], float2 (&z)[N], const
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
     group_norm_bwd_kernel(GroupNormArgs a, RowPlan p) {
+  after_previous();
+  let_next();
   constexpr int E = VEC * NV, N = E / 2;  // elements and pairs of a lane
   constexpr int kPerBlock = kRowThreads / L;
   const int lane = threadIdx.x % L;
@@ -181,7 +183,6 @@ __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV))
   // Partial rows of the weight gradients, a block's D values each, db behind dw:
   // over the slots of a warp, then over the warps.
   if (!a.dweight && !a.dbias) return;
-  let_next();
   Sums &s = *reinterpret_cast<Sums *>(memory);  // (no request is left)
   const int warp = threadIdx.x / 32, at = threadIdx.x % 32;
 #pragma unroll
@@ -231,15 +232,14 @@ struct Launch {
   template <typename T, int VEC, int L, int NV>
   cudaError_t operator()() const {
     const RowPlan p = bwd_plan(a.rows, a.G, L, blocks_per_sm(VEC * NV), a.per_channel);
-    group_norm_bwd_kernel<T, VEC, L, NV><<<p.blocks, kRowThreads, 0, stream>>>(a, p);
-    if (p.sum && (a.dweight || a.dbias)) {
-      const cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
+    const cudaError_t e =
+        launch_next(group_norm_bwd_kernel<T, VEC, L, NV>, dim3(p.blocks), kRowThreads, stream, a, p);
+    if (e == cudaSuccess && p.sum && (a.dweight || a.dbias)) {
       const int rows = a.per_channel ? p.blocks / a.G : p.blocks;
       const int cols = a.per_channel ? a.G * a.D : a.D;
       return launch_sums(a.ws, rows, cols, a.dweight, a.dbias, stream);
     }
-    return cudaGetLastError();
+    return e;
   }
 };
 

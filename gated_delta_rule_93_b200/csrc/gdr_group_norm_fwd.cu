@@ -29,6 +29,8 @@ __device__ __forceinline__ void finish(float2 (&x)[N], const float2 (&z)[N], con
 template <typename T, int VEC, int L, int NV>
 __global__ void __launch_bounds__(kRowThreads, blocks_per_sm(VEC *NV, VEC))
     group_norm_fwd_kernel(GroupNormArgs a, RowPlan p) {
+  after_previous();
+  let_next();
   constexpr int E = VEC * NV, N = E / 2;  // elements and pairs of a lane
   constexpr int kPerBlock = kRowThreads / L;
   const int lane = threadIdx.x % L;
@@ -129,8 +131,8 @@ struct Launch {
   cudaError_t operator()() const {
     const RowPlan p =
         row_plan(a.rows, a.G, kRowThreads / L, kTurns, kSMs * blocks_per_sm(VEC * NV, VEC), false);
-    group_norm_fwd_kernel<T, VEC, L, NV><<<p.blocks, kRowThreads, 0, stream>>>(a, p);
-    return cudaGetLastError();
+    return launch_next(group_norm_fwd_kernel<T, VEC, L, NV>, dim3(p.blocks), kRowThreads, stream, a,
+                       p);
   }
 };
 

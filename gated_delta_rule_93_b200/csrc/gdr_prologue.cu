@@ -185,6 +185,8 @@ __device__ __forceinline__ void gates_bwd(const PrologueArgs &a, const GatePlan 
 
 template <typename T, int VEC, int L>
 __global__ void __launch_bounds__(kRowThreads, 4) prologue_fwd_kernel(PrologueArgs a, Split p) {
+  after_previous();
+  let_next();
   const int block = blockIdx.x;
   if (block >= p.norm.blocks) {
     gates_fwd(a, p.gate, block - p.norm.blocks);
@@ -236,6 +238,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) prologue_fwd_kernel(PrologueAr
 
 template <typename T, int VEC, int L>
 __global__ void __launch_bounds__(kRowThreads, 4) prologue_bwd_kernel(PrologueArgs a, Split p) {
+  after_previous();
+  let_next();
   const int block = blockIdx.x;
   if (block >= p.norm.blocks) {
     gates_bwd(a, p.gate, block - p.norm.blocks);
@@ -293,16 +297,14 @@ cudaError_t launch_one(const PrologueArgs &a, cudaStream_t stream) {
                    gate_plan(a.tokens, a.H, a.d, a.per_channel)};
   const int blocks = p.norm.blocks + p.gate.blocks;
   if constexpr (!BWD) {
-    prologue_fwd_kernel<T, VEC, L><<<blocks, kRowThreads, 0, stream>>>(a, p);
+    return launch_next(prologue_fwd_kernel<T, VEC, L>, dim3(blocks), kRowThreads, stream, a, p);
   } else {
-    prologue_bwd_kernel<T, VEC, L><<<blocks, kRowThreads, 0, stream>>>(a, p);
-    if (p.gate.blocks > p.gate.tiles) {
-      const cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
+    const cudaError_t e =
+        launch_next(prologue_bwd_kernel<T, VEC, L>, dim3(blocks), kRowThreads, stream, a, p);
+    if (e == cudaSuccess && p.gate.blocks > p.gate.tiles)
       return launch_sums(a.ws, p.gate.blocks / p.gate.tiles, a.H, a.dgate_scale, nullptr, stream);
-    }
+    return e;
   }
-  return cudaGetLastError();
 }
 
 template <bool BWD, typename T, int VEC>

@@ -248,8 +248,11 @@ __device__ __forceinline__ float softplus(float x, float *sig = nullptr) {
   return y.x;
 }
 
-// Launches `kernel` so that it may be set up while the one before it ends; it has to
-// begin with after_previous().
+// Launches `kernel` so that its blocks may be set up while the kernel before it
+// on the stream ends.  It has to begin, in every thread, with after_previous(),
+// which waits until that kernel is done and its writes are seen: nothing is
+// read or written earlier, so the order on the stream is the ordinary one.
+// let_next() tells that the kernel behind may be set up in turn.
 template <typename... P, typename... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t config = {};

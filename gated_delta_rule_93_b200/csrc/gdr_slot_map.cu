@@ -7,7 +7,7 @@
 // shared memory.  The entries behind the last token are split over all blocks.  The
 // work is a few KB: the launch and two dependent reads from memory bound it (3 us
 // for a few requests, where an empty kernel takes 2).
-#include "gdr_internal.cuh"
+#include "gdr_rows.cuh"
 
 namespace gdr {
 namespace {
@@ -26,6 +26,8 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 }
 
 __global__ void __launch_bounds__(kThreads) gdr_slot_map_kernel(SlotMapArgs a, int own) {
+  after_previous();
+  let_next();
   constexpr int kWarps = kThreads / 32;
   __shared__ long long s_all[kWarps], s_before[kWarps], s_scan[kWarps];
   __shared__ int s_cu[kThreads + 1];
@@ -141,8 +143,7 @@ __global__ void __launch_bounds__(kThreads) gdr_slot_map_kernel(SlotMapArgs a, i
 cudaError_t launch_slot_map(const SlotMapArgs &a, cudaStream_t stream) {
   const int own = a.R <= kFewRequests ? kThreads / 4 : kThreads;
   const int blocks = a.R > 0 ? (a.R + own - 1) / own : 1;
-  gdr_slot_map_kernel<<<blocks, kThreads, 0, stream>>>(a, own);
-  return cudaGetLastError();
+  return launch_next(gdr_slot_map_kernel, dim3(blocks), kThreads, stream, a, own);
 }
 
 }  // namespace gdr

@@ -126,6 +126,8 @@ __device__ __forceinline__ float reduce8(float (&x)[8], int lane) {
 template <int DK, int WARPS, bool BF16, bool PERCH>
 __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 32) / WARPS)
     gdr_step_slots_kernel(StepSlotsArgs a) {
+  after_previous();
+  let_next();
   constexpr int kRows = rows_of(WARPS);
   constexpr int NC = DK / 32;  // float4s of a row per lane
   __shared__ Prepared<DK, WARPS, PERCH> sm;
@@ -290,6 +292,8 @@ __global__ void __launch_bounds__(WARPS * 32, (DK == 128 ? 16 : DK == 64 ? 24 : 
 // nothing waits at a barrier, and a warp's stores leave while others load.
 template <int DK, bool BF16, bool PERCH>
 __global__ void __launch_bounds__(128, 7) gdr_step_slots_one_kernel(StepSlotsArgs a) {
+  after_previous();
+  let_next();
   constexpr int VEC = DK / 32, kRows = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks_per_head = a.dv / (4 * kRows);
@@ -407,19 +411,11 @@ template <int DK, int WARPS>
 cudaError_t launch_warps(const StepSlotsArgs &a, cudaStream_t stream) {
   const size_t blocks = (size_t)a.R * a.H * (a.dv / rows_of(WARPS));
   if (blocks > 0x7fffffffu) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(WARPS * 32);
-  if (a.bf16) {
-    if (a.per_channel)
-      gdr_step_slots_kernel<DK, WARPS, true, true><<<grid, block, 0, stream>>>(a);
-    else
-      gdr_step_slots_kernel<DK, WARPS, true, false><<<grid, block, 0, stream>>>(a);
-  } else {
-    if (a.per_channel)
-      gdr_step_slots_kernel<DK, WARPS, false, true><<<grid, block, 0, stream>>>(a);
-    else
-      gdr_step_slots_kernel<DK, WARPS, false, false><<<grid, block, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+  const auto kernel = a.bf16 ? (a.per_channel ? gdr_step_slots_kernel<DK, WARPS, true, true>
+                                              : gdr_step_slots_kernel<DK, WARPS, true, false>)
+                             : (a.per_channel ? gdr_step_slots_kernel<DK, WARPS, false, true>
+                                              : gdr_step_slots_kernel<DK, WARPS, false, false>);
+  return launch_next(kernel, dim3((unsigned)blocks), WARPS * 32, stream, a);
 }
 
 template <int DK>
@@ -427,19 +423,11 @@ cudaError_t launch_dk(const StepSlotsArgs &a, cudaStream_t stream) {
   if (!a.cu) {
     const size_t blocks = (size_t)a.R * a.H * (a.dv / 32);
     if (blocks > 0x7fffffffu) return cudaErrorInvalidValue;
-    const unsigned n = (unsigned)blocks;
-    if (a.bf16) {
-      if (a.per_channel)
-        gdr_step_slots_one_kernel<DK, true, true><<<n, 128, 0, stream>>>(a);
-      else
-        gdr_step_slots_one_kernel<DK, true, false><<<n, 128, 0, stream>>>(a);
-    } else {
-      if (a.per_channel)
-        gdr_step_slots_one_kernel<DK, false, true><<<n, 128, 0, stream>>>(a);
-      else
-        gdr_step_slots_one_kernel<DK, false, false><<<n, 128, 0, stream>>>(a);
-    }
-    return cudaGetLastError();
+    const auto kernel = a.bf16 ? (a.per_channel ? gdr_step_slots_one_kernel<DK, true, true>
+                                                : gdr_step_slots_one_kernel<DK, true, false>)
+                               : (a.per_channel ? gdr_step_slots_one_kernel<DK, false, true>
+                                                : gdr_step_slots_one_kernel<DK, false, false>);
+    return launch_next(kernel, dim3((unsigned)blocks), 128, stream, a);
   }
   constexpr int kWarps = 4;
   return a.dv == 32 ? launch_warps<DK, 2>(a, stream) : launch_warps<DK, kWarps>(a, stream);
