@@ -227,6 +227,15 @@ class Call {
   bool other_ = false;
 };
 
+// n elements of a new one-dimensional tensor's memory, from `at` on.
+at::Tensor piece(const at::Tensor &whole, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()),
+                                                          whole.key_set(), whole.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 PyObject *wrap(const at::Tensor &t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -363,10 +372,10 @@ PyObject *slot_map(PyObject *, PyObject *const *x, Py_ssize_t n) {
     at::Tensor cu, src, request, dst;
     if (x[6] == Py_None) {  // four pieces of one allocation
       const at::Tensor all = call.make({2 * R + 1 + 2 * room}, at::kInt);
-      cu = all.as_strided({R + 1}, {1}, 0);
-      src = all.as_strided({R}, {1}, R + 1);
-      request = all.as_strided({room}, {1}, 2 * R + 1);
-      dst = all.as_strided({room}, {1}, 2 * R + 1 + room);
+      cu = piece(all, 0, R + 1);
+      src = piece(all, R + 1, R);
+      request = piece(all, 2 * R + 1, room);
+      dst = piece(all, 2 * R + 1 + room, room);
     } else {
       cu = call.given_or_made(entry(x[6], "cu_seqlens"), "cu_seqlens", {R + 1}, at::kInt);
       src = call.given_or_made(entry(x[6], "src"), "src", {R}, at::kInt);
