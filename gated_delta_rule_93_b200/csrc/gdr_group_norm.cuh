@@ -9,7 +9,7 @@
 //
 // A lane keeps the same group index for all its rows (the number of groups
 // in flight is a multiple of G), so its weights are loaded once and addresses
-// advance by a constant.  A block takes few rows a lane (8 forward, 16 backward): with
+// advance by a constant.  A block takes few rows a lane (8, or 16): with
 // a grid that fills the SMs once and runs to the end, the slowest SM sets the
 // time (forward of 32768 x 16 x 128 bf16: 74.7 us, with 8 rows 62.4 us, with 1 row,
 // where blocks spend their time on starting, 121 us).
@@ -19,7 +19,7 @@
 // what HBM leaves time for (the forward issues on 77 % of the cycles).
 //
 // 32768 x 16 x 128 bf16, SiLU gate: forward 62.4 us (6447 GB/s; a copy runs at 6456),
-// gradient 131.7 us (6116 GB/s, its second launch included).  Groups that do not start
+// gradient 130.9 us (6151 GB/s, its second launch included).  Groups that do not start
 // on 16 bytes: 32768 x 16 x 100 bf16 (8-byte accesses) forward 62.4 us (5044 GB/s), 31 x 33
 // (2-byte accesses, bound by instructions) 74.2 us (2712 GB/s), gradient 178 us.
 #pragma once
