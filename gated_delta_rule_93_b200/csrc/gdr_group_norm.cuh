@@ -21,7 +21,7 @@
 // 32768 x 16 x 128 bf16, SiLU gate: forward 62.4 us (6447 GB/s; a copy runs at 6456),
 // gradient 130.9 us (6151 GB/s, its second launch included).  Groups that do not start
 // on 16 bytes: 32768 x 16 x 100 bf16 (8-byte accesses) forward 62.4 us (5044 GB/s), 31 x 33
-// (2-byte accesses, bound by instructions) 74.2 us (2712 GB/s), gradient 178 us.
+// (2-byte accesses, bound by instructions) 66.4 us (3030 GB/s), gradient 169 us.
 #pragma once
 
 #include "gdr_rows.cuh"
@@ -106,7 +106,7 @@ constexpr bool norm_queue = sizeof(Raw<T, VEC>) >= 8 && NV <= 2;
 // accesses: one a lane where they fit, so that most rows are in flight.  Narrower
 // ones are bound by instructions, most of them the same for every group of a
 // warp: several accesses a lane and fewer lanes a group (33 channels of bf16, 1 M
-// groups: 32 lanes of 2 elements 194 us, 8 lanes of 8 elements 89 us).
+// groups: 32 lanes of 2 elements 194 us, 8 lanes of 6 elements 66 us).
 template <typename T, int VEC, typename F>
 cudaError_t norm_layout_vec(int D, F f) {
   const int n = (D + VEC - 1) / VEC;  // accesses of a group
@@ -127,9 +127,14 @@ cudaError_t norm_layout_vec(int D, F f) {
     if (n <= 128) return f.template operator()<T, VEC, 32, 4>();
     if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
   } else {
+    // (6 or 8 accesses a lane: the fewer, the less of a short group's lanes are idle)
+    if (n <= 24) return f.template operator()<T, VEC, 4, 6>();
     if (n <= 32) return f.template operator()<T, VEC, 4, 8>();
+    if (n <= 48) return f.template operator()<T, VEC, 8, 6>();
     if (n <= 64) return f.template operator()<T, VEC, 8, 8>();
+    if (n <= 96) return f.template operator()<T, VEC, 16, 6>();
     if (n <= 128) return f.template operator()<T, VEC, 16, 8>();
+    if (n <= 192) return f.template operator()<T, VEC, 32, 6>();
     if (n <= 256) return f.template operator()<T, VEC, 32, 8>();
     if (n <= 512) return f.template operator()<T, VEC, 32, 16>();
     if (n <= 640) return f.template operator()<T, VEC, 32, 20>();

@@ -93,8 +93,8 @@ def test_forms(cuda_device, dtype, act, gated, center, affine):
 
 
 # one element, below and above a vector, odd, every number of vectors a lane holds, the widest
-@pytest.mark.parametrize("D", [1, 2, 7, 8, 20, 31, 32, 33, 48, 64, 80, 96, 100, 192, 250, 256, 257,
-                               500, 512, 513, 1000, 1023, 1024])
+@pytest.mark.parametrize("D", [1, 2, 7, 8, 20, 31, 32, 33, 48, 63, 64, 80, 95, 96, 100, 127, 191, 192,
+                               250, 252, 255, 256, 257, 500, 512, 513, 1000, 1020, 1023, 1024])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("affine", ["group", "channel"])
 def test_widths(cuda_device, D, dtype, affine):
