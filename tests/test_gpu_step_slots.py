@@ -96,6 +96,24 @@ def test_one_token_in_place(cuda_device, dtype, gate, dk, dv, raw):
     assert np.array_equal(f64(d["pool"])[untouched], rp[untouched])
 
 
+@pytest.mark.parametrize("gate", ["scalar", "channel"])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+def test_many_small_states(cuda_device, gate, dv):
+    """Keys of 32 channels and more rows than the one-token kernel takes: the same
+    step through the other kernel, skipped and new requests among them."""
+    R, H = 16384 // (4 * dv) + 3, 4
+    d = make([1] * R, 2, H, 32, dv, torch.bfloat16, gate, True, slots=R + 5, seed=dv)
+    src = torch.randperm(R + 5, generator=torch.Generator().manual_seed(1))[:R].int().cuda()
+    src[3], src[7] = SLOT_SKIP, SLOT_ZERO
+    o = torch.full_like(d["v"], 3.0)
+    ro, rp = expect(d, src, cu=False, o=o)
+    call(d, src, cu=False, o=o)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0 and (o[3] == 3.0).all()
+    close(o, ro, tolerance(32, 1, torch.bfloat16), "o")
+    close(d["pool"], rp, tolerance(32, 1), "pool")
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("gate", ["scalar", "channel"])
 @pytest.mark.parametrize("fused", [True, False])
