@@ -97,7 +97,7 @@ __device__ __forceinline__ float normalise(float2 (&x)[VEC * NV / 2], const bool
   return rsqrtf(lanes_sum<L>(ss.x + ss.y) * inv_d + eps);
 }
 
-// Whether a layout's rows wait in shared memory, and how many bytes of a row a lane reads.
+// Whether a layout's rows wait in shared memory.
 template <typename T, int VEC, int NV>
 constexpr bool norm_queue = sizeof(Raw<T, VEC>) >= 8 && NV <= 2;
 

@@ -1,5 +1,6 @@
-// Helpers of the row-wise kernels (output norm, prologue): vectors of
-// elements, sums over the lanes that share a row, sums of partial rows.
+// Helpers of the kernels around the mixer (pooled decode, slot map, output
+// norm, prologue): vectors and pairs of elements, sums over the lanes that share
+// a row, sums of partial rows, launches that overlap the kernel before them.
 #pragma once
 
 #include <cooperative_groups.h>

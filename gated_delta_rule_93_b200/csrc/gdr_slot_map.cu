@@ -110,11 +110,12 @@ __global__ void __launch_bounds__(kThreads) gdr_slot_map_kernel(SlotMapArgs a, i
   }
   __syncthreads();
 
-  for (int t = s_cu[0] + tid; t < s_cu[own]; t += kThreads) {
+  // (unsigned: the step behind the last of 2^31 - 1 tokens does not wrap)
+  for (unsigned t = s_cu[0] + tid; t < (unsigned)s_cu[own]; t += kThreads) {
     int lo = 0, hi = own;  // s_cu[lo] <= t < s_cu[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_cu[mid] <= t)
+      if ((unsigned)s_cu[mid] <= t)
         lo = mid;
       else
         hi = mid;
