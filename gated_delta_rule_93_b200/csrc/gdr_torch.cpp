@@ -177,11 +177,14 @@ int fits(int64_t v, const char *name) {
 }
 
 // The device of a call made current, its stream, and what it allocates: from
-// the current stream's memory, kept until the call's own stream is done with it.
+// the memory of the call's own stream, on which alone the order of a block's last
+// user and of the kernel that writes it next is given; what the caller gets is
+// kept, once freed, until the current stream is done with it too.
 class Call {
  public:
   Call(c10::Device device, PyObject *stream)
-      : guard_(device), stream_(c10::cuda::getCurrentCUDAStream(device.index())) {
+      : guard_(device), stream_(c10::cuda::getCurrentCUDAStream(device.index())),
+        caller_(stream_) {
     if (stream == Py_None) return;
     if (!THPStream_Check(stream)) refuse(PyExc_TypeError, "stream must be a torch.cuda.Stream");
     const auto *s = reinterpret_cast<THPStream *>(stream);
@@ -191,14 +194,14 @@ class Call {
              (long long)s->device_index, device.str().c_str());
     const auto given = c10::cuda::CUDAStream(
         c10::Stream::unpack3(s->stream_id, s->device_index, c10::DeviceType::CUDA));
-    other_ = given != stream_;
     stream_ = given;
   }
 
   at::Tensor make(at::IntArrayRef size, at::ScalarType type) {
-    // (as at::empty, without its way through the dispatcher: 1 us of 2)
-    at::Tensor t = at::detail::empty_cuda(size, type, guard_.current_device(), std::nullopt);
-    if (other_ && t.numel()) t.record_stream(stream_.unwrap());
+    if (stream_ == caller_) return empty(size, type);
+    const c10::cuda::CUDAStreamGuard of_the_call(stream_);
+    at::Tensor t = empty(size, type);
+    if (t.numel()) t.record_stream(caller_.unwrap());
     return t;
   }
 
@@ -222,9 +225,13 @@ class Call {
   gdr_stream_t stream() const { return reinterpret_cast<gdr_stream_t>(stream_.stream()); }
 
  private:
+  at::Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
+    // (as at::empty, without its way through the dispatcher: 1 us of 2)
+    return at::detail::empty_cuda(size, type, guard_.current_device(), std::nullopt);
+  }
+
   c10::cuda::CUDAGuard guard_;
-  c10::cuda::CUDAStream stream_;
-  bool other_ = false;
+  c10::cuda::CUDAStream stream_, caller_;  // the call's, and the one that is current
 };
 
 // n elements of a new one-dimensional tensor's memory, from `at` on.
