@@ -163,6 +163,19 @@ def _stream_handle(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(size, dtype, dev, stream):
+    """Memory for a call on ``stream``: that stream's own, whose order alone says when a
+    block's last user is done; kept, once freed, until the current stream is done with it."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):  # (anything with a stream handle)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(size, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _need(t, name, dtype=None, shape=None, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -222,10 +235,10 @@ def chunk_fwd(q, k, v, g, beta, S0=None, *, output_final_state=True, o=None, S_T
     if S0 is not None:
         _need(S0, "S0", torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = _empty((B, T, H, dv), dt, dev, stream)
     _need(o, "o", dt, (B, T, H, dv), dev)
     if output_final_state and S_T is None:
-        S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        S_T = _empty((B, H, dv, dk), torch.float32, dev, stream)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, (B, H, dv, dk), dev)
     with torch.cuda.device(dev):
@@ -233,7 +246,7 @@ def chunk_fwd(q, k, v, g, beta, S0=None, *, output_final_state=True, o=None, S_T
         # library reads from the current device
         ws = chunk_fwd_workspace_bytes(B, T, H, dk, dv, C, dt, "channel" if gk else "scalar")
         if ws and workspace is None:
-            workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+            workspace = _empty(ws, torch.uint8, dev, stream)
         rc = lib().gdr_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _in_dtype(dt), _ptr(g), gk,
                                  _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T), B, T, H, dk, dv, C,
                                  _ptr(workspace), workspace.numel() if workspace is not None
@@ -263,7 +276,7 @@ def step(q, k, v, g, beta, S, *, o=None, stream=None):
     _need(beta, "beta", torch.float32, (N, H), dev)
     _need(S, "S", torch.float32, (N, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((N, H, dv), dtype=dt, device=dev)
+        o = _empty((N, H, dv), dt, dev, stream)
     _need(o, "o", dt, (N, H, dv), dev)
     with torch.cuda.device(dev):
         rc = lib().gdr_step(_ptr(q), _ptr(k), _ptr(v), _in_dtype(dt), _ptr(g), gk, _ptr(beta),
@@ -307,10 +320,10 @@ def chunk_fwd_segmented(q, k, v, g, beta, S0=None, *, segments, workspace,
     if not isinstance(workspace, torch.Tensor) or workspace.device != dev:
         raise ValueError("workspace must be a tensor on the inputs' device")
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = _empty((B, T, H, dv), dt, dev, stream)
     _need(o, "o", dt, (B, T, H, dv), dev)
     if output_final_state and S_T is None:
-        S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        S_T = _empty((B, H, dv, dk), torch.float32, dev, stream)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, (B, H, dv, dk), dev)
     with torch.cuda.device(dev):
@@ -390,10 +403,10 @@ def chunk_fwd_varlen(q, k, v, g, beta, cu_seqlens, S0=None, *, output_final_stat
     if S0 is not None:
         _need(S0, "S0", torch.float32, (N, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((total, H, dv), dtype=dt, device=dev)
+        o = _empty((total, H, dv), dt, dev, stream)
     _need(o, "o", dt, (total, H, dv), dev)
     if output_final_state and S_T is None:
-        S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        S_T = _empty((N, H, dv, dk), torch.float32, dev, stream)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
     with torch.cuda.device(dev):
@@ -426,10 +439,10 @@ def chunk_fwd_gla(q, k, v, g, S0=None, *, output_final_state=True, o=None, S_T=N
     if S0 is not None:
         _need(S0, "S0", torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = _empty((B, T, H, dv), dt, dev, stream)
     _need(o, "o", dt, (B, T, H, dv), dev)
     if output_final_state and S_T is None:
-        S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        S_T = _empty((B, H, dv, dk), torch.float32, dev, stream)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, (B, H, dv, dk), dev)
     with torch.cuda.device(dev):
@@ -467,10 +480,10 @@ def chunk_fwd_prologue(q, k, v, a, b, gate_scale, S0=None, *, norm_q=True, norm_
     if S0 is not None:
         _need(S0, "S0", torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = _empty((B, T, H, dv), dt, dev, stream)
     _need(o, "o", dt, (B, T, H, dv), dev)
     if output_final_state and S_T is None:
-        S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        S_T = _empty((B, H, dv, dk), torch.float32, dev, stream)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, (B, H, dv, dk), dev)
     flags = (1 if norm_q else 0) | (2 if norm_k else 0)
@@ -515,12 +528,11 @@ def chunk_bwd(q, k, v, g, beta, dout, S0=None, dS_T=None, *, want_dS0=True, work
         _need(S0, "S0", torch.float32, (B, H, dv, dk), dev)
     if dS_T is not None:
         _need(dS_T, "dS_T", torch.float32, (B, H, dv, dk), dev)
-    f32 = dict(dtype=torch.float32, device=dev)
     if out is None:  # (or the caller's preallocated dict of the same tensors)
-        out = dict(dq=torch.empty((B, T, H, dk), **f32), dk=torch.empty((B, T, H, dk), **f32),
-                   dv=torch.empty((B, T, H, dv), **f32), dg=torch.empty(tuple(g.shape), **f32),
-                   dbeta=torch.empty((B, T, H), **f32),
-                   dS0=torch.empty((B, H, dv, dk), **f32) if want_dS0 else None)
+        made = lambda *size: _empty(size, torch.float32, dev, stream)  # noqa: E731
+        out = dict(dq=made(B, T, H, dk), dk=made(B, T, H, dk), dv=made(B, T, H, dv),
+                   dg=made(*g.shape), dbeta=made(B, T, H),
+                   dS0=made(B, H, dv, dk) if want_dS0 else None)
     for name, shape in (("dq", (B, T, H, dk)), ("dk", (B, T, H, dk)), ("dv", (B, T, H, dv)),
                         ("dg", tuple(g.shape)), ("dbeta", (B, T, H))):
         _need(out[name], name, torch.float32, shape, dev)
@@ -528,7 +540,7 @@ def chunk_bwd(q, k, v, g, beta, dout, S0=None, dS_T=None, *, want_dS0=True, work
         _need(out["dS0"], "dS0", torch.float32, (B, H, dv, dk), dev)
     ws = chunk_bwd_workspace_bytes(B, T, H, dk, dv, dt, "channel" if gk else "scalar")
     if workspace is None and ws:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws, torch.uint8, dev, stream)
     with torch.cuda.device(dev):
         rc = lib().gdr_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _in_dtype(dt), _ptr(g), gk,
                                  _ptr(beta), _ptr(S0), _ptr(dout), _ptr(dS_T), _ptr(out["dq"]),
@@ -563,10 +575,10 @@ def dplr_fwd(q, k, v, a, b, g, S0=None, *, output_final_state=True, o=None, S_T=
     if S0 is not None:
         _need(S0, "S0", torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = _empty((B, T, H, dv), dt, dev, stream)
     _need(o, "o", dt, (B, T, H, dv), dev)
     if output_final_state and S_T is None:
-        S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        S_T = _empty((B, H, dv, dk), torch.float32, dev, stream)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, (B, H, dv, dk), dev)
     with torch.cuda.device(dev):
