@@ -650,7 +650,8 @@ def slot_map(lens, kept, table, slots, max_tokens, *, keep_all=True, out=None, s
     is the size of the pool, ``max_tokens`` the room for tokens.  Returns a
     dict of int32 tensors: cu_seqlens [R+1], src [R], request and dst
     [max_tokens] (see ``step_slots``; -1 behind the last token), pieces of one
-    allocation unless ``out`` is such a dict.
+    allocation unless ``out`` is such a dict (where an entry is None, what is
+    made for it is put there).
     """
     r = (_native or native()).slot_map(lens, kept, table, slots, max_tokens, keep_all, out, stream)
     if type(r) is int:
@@ -679,8 +680,10 @@ def group_norm_bwd(dy, x, z=None, weight=None, bias=None, *, act="silu", center=
 
     dy as x, contiguous.  Returns dict dx (fp32, what ``chunk_bwd`` takes as
     dout), dz (dtype of z), dweight, dbias (fp32); what has no input is None.
-    ``out`` may be such a dict, preallocated; ``workspace`` a CUDA tensor of
-    ``gdr_group_norm_bwd_workspace_bytes`` (calls that overlap need one each).
+    ``out`` may be such a dict, preallocated: it is returned, with what was made
+    for entries that were None; entries without an input stay as they are.
+    ``workspace`` may be a CUDA tensor of ``gdr_group_norm_bwd_workspace_bytes``
+    (calls that overlap need one each).
     """
     r = (_native or native()).group_norm_bwd(x, z, weight, bias, _act(act), center, eps, dy,
                                              workspace, out, stream)
@@ -697,7 +700,7 @@ def prologue_fwd(q, k, a, b, gate_scale, *, norm_q=True, norm_k=True, out=None, 
     or [..., H, dk] and b [..., H] fp32 logits; gate_scale [H] fp32.  q, k come
     back normalised (per the flags) with one copy for each of the H value
     heads; g = -gate_scale softplus(a), beta = sigmoid(b).  ``out`` may be the
-    preallocated tuple of them.
+    preallocated tuple of them (None: made here).
     """
     r = (_native or native()).prologue_fwd(q, k, a, b, gate_scale, norm_q, norm_k, out, stream)
     if type(r) is int:

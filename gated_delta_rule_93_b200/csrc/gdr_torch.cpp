@@ -254,14 +254,18 @@ PyObject *entry(PyObject *dict, const char *name) {
   return v;
 }
 
+// A call's results: a new dict, or the caller's, whose entries that were None become the
+// tensors made for them.
 PyObject *dictionary(PyObject *given,
                      std::initializer_list<std::pair<const char *, const at::Tensor &>> items) {
-  if (given != Py_None) {
+  PyObject *d = given;
+  if (given == Py_None)
+    d = PyDict_New();
+  else
     Py_INCREF(given);
-    return given;
-  }
-  PyObject *d = PyDict_New();
   for (const auto &it : items) {
+    if (d == given && !(it.second.defined() && PyDict_GetItemString(d, it.first) == Py_None))
+      continue;
     PyObject *v = wrap(it.second);
     PyDict_SetItemString(d, it.first, v);
     Py_DECREF(v);
