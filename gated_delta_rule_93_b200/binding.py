@@ -13,13 +13,17 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sysconfig
 import threading
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
-NATIVE_PATH = os.path.join(_HERE, "_gdr_torch.so")
+# The front end uses torch's C++ interfaces: its name says which torch and Python it is of, so
+# that one of another is never loaded (or taken for up to date by the build).
+NATIVE_PATH = os.path.join(_HERE, "_gdr_torch.%s-%s%s" % (
+    torch.__version__, (torch.version.git_version or "")[:8], sysconfig.get_config_var("EXT_SUFFIX")))
 _lib = None
 _native = None
 _lock = threading.Lock()

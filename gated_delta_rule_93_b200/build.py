@@ -1,5 +1,6 @@
 """Build ``libgdr.so`` (the C-ABI library) in-tree with nvcc for sm_100a, and
-``_gdr_torch.so`` (the compiled torch front end of some of its entry points).
+the compiled torch front end of some of its entry points (``_gdr_torch*.so``,
+named after the torch and Python it is for).
 
 Usage: ``python -m gated_delta_rule_93_b200.build [--force] [-v]``.
 Each ``csrc/*.cu`` compiles to ``_build/*.o`` in parallel (skipped when the
@@ -20,13 +21,14 @@ import subprocess
 import sys
 import warnings
 
+from .binding import NATIVE_PATH as NATIVE
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr.so")
-NATIVE = os.path.join(PKG, "_gdr_torch.so")
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

@@ -1,6 +1,8 @@
 """What a build leaves behind where a part of its tools is missing (no GPU, no compiler run)."""
 import os
 import stat
+import subprocess
+import sys
 
 import pytest
 
@@ -45,3 +47,29 @@ def test_a_failing_kernel_source_is_an_error(tree, monkeypatch):
     with pytest.raises(RuntimeError, match="nvcc failed"):
         B.build(force=True)
     assert not os.path.exists(B.LIB)
+
+
+OTHER = """
+import sys
+import torch
+{change}
+from gated_delta_rule_93_b200 import binding
+try:
+    binding.native()
+except RuntimeError as e:
+    sys.exit(0 if "missing" in str(e) else 2)
+sys.exit(1)  # loaded
+"""
+
+
+@pytest.mark.parametrize("change,loads", [
+    ("", True), ("torch.__version__ = '2.99.0'", False),
+    ("torch.version.git_version = '0123456789abcdef'", False),
+    ("import sysconfig; sysconfig.get_config_vars()['EXT_SUFFIX'] = '.cpython-399-other.so'", False)])
+def test_a_front_end_of_another_torch_is_not_loaded(change, loads):
+    """The front end uses torch's C++ interfaces: what was compiled against another torch or
+    Python is not this one's, whatever its file times say."""
+    B.build()
+    r = subprocess.run([sys.executable, "-c", OTHER.format(change=change)], cwd=B.ROOT,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == (1 if loads else 0), r.stderr
