@@ -14,6 +14,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -226,7 +227,10 @@ class Call {
 
  private:
   at::Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
-    // (as at::empty, without its way through the dispatcher: 1 us of 2)
+    // at::empty's own way where somebody looks at it (a dispatch mode) or fills new memory;
+    // else without the dispatcher: 1 us of 2.
+    if (c10::impl::dispatch_mode_enabled() || at::globalContext().deterministicAlgorithms())
+      return at::empty(size, at::TensorOptions(type).device(guard_.current_device()));
     return at::detail::empty_cuda(size, type, guard_.current_device(), std::nullopt);
   }
 
