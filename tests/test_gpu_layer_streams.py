@@ -126,3 +126,45 @@ def test_captured_on_a_stream_of_its_own(batch):
         torch.cuda.synchronize()
         assert all(torch.equal(got[n], want[n]) for n in ("dx", "dz", "dweight"))
         assert torch.equal(double, want["dx"] * 2) and torch.isnan(junk).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_events_of_other_streams_are_waited_for(batch, captured):
+    """Kernels that are set up while the one before them on their stream ends wait all the
+    same for an event of another stream that lies between the two."""
+    x, w, _ = batch
+    start = x.clone()
+    for _ in range(PASSES):
+        start.add_(1.0)
+    first, want = binding.group_norm_fwd(x, None, w), binding.group_norm_fwd(start, None, w)
+    q, a, s = x.view(-1, 16, 128)[:, :2], torch.zeros(ROWS, 16, device="cuda"), torch.ones(16, device="cuda")
+    want_q = binding.prologue_fwd(start[:, :2], start[:, :2], a, a, s)[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    keep = x.clone()
+
+    def work():
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        y0 = binding.group_norm_fwd(x, None, w, stream=side)  # (of x as it was)
+        now.wait_stream(side)
+        long_chain(x)
+        y1 = binding.group_norm_fwd(start, None, w, stream=side)  # a kernel right before
+        side.wait_stream(now)
+        y2 = binding.group_norm_fwd(x, None, w, stream=side)
+        side.wait_stream(now)
+        y3 = binding.prologue_fwd(q, q, a, a, s, stream=side)[0]
+        now.wait_stream(side)
+        return y0, y1, y2, y3
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = work()
+        for _ in range(2):
+            x.copy_(keep)
+            graph.replay()
+    else:
+        got = work()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, t) for g, t in zip(got, (first, want, want, want_q)))
