@@ -15,8 +15,8 @@
 // where blocks spend their time on starting, 121 us).
 //
 // Arithmetic is in pairs of fp32 and on the fast exponential and reciprocal: a
-// gated SiLU takes 23 instructions an element forward and 31 backward (counted), just
-// what HBM leaves time for (the forward issues on 77 % of the cycles).
+// gated SiLU takes 23 instructions an element forward and 34 backward (counted), just
+// what HBM leaves time for (the forward issues on 78 % of the cycles).
 //
 // 32768 x 16 x 128 bf16, SiLU gate: forward 62.4 us (6447 GB/s; a copy runs at 6456),
 // gradient 130.9 us (6151 GB/s, its second launch included).  Groups that do not start

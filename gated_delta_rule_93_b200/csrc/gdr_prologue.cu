@@ -20,7 +20,7 @@
 // 32768 tokens, bf16, scalar gates, 8 key heads of 128 for 16 value heads: forward
 // 64.8 us (6347 GB/s; a copy runs at 6456), gradient 128.7 us (6353 GB/s).
 // Per-channel gates spend a third of their time on softplus and sigmoid: 8192
-// tokens x 16 x 128 forward 48.8 us (5521 GB/s), gradient 83.3 us (5659 GB/s).  The
+// tokens x 16 x 128 forward 48.8 us (5521 GB/s), gradient 82.5 us (5712 GB/s).  The
 // gradient takes q, then k, so that 64 registers do and four blocks fit an SM (both
 // at once, three blocks: 131.1 and 91.0 us).
 #include "gdr_rows.cuh"

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256;
 // Up to here a block owns 64 requests, so that four threads share a request's
-// tokens (4096 requests of 0 to 8 tokens: 4.4 us, with 256 a block 5.7 us); beyond,
+// tokens (4096 requests of 0 to 8 tokens: 4.1 us, with 256 a block 5.6 us); beyond,
 // 256, since every block reads all lengths.
 constexpr int kFewRequests = 8192;
 constexpr int kAhead = 8;  // lengths a thread asks for at once
